@@ -199,7 +199,7 @@ def prepare(case, seed):
         st["ids"] = torch.empty((M, k), dtype=torch.int32, device=dev)
         st["rw"] = torch.empty((M, k), dtype=_DT[c["rw"]], device=dev)
         if c["train"]:
-            st["lse"] = torch.empty(M, dtype=torch.float32, device=dev)
+            st["stats"] = torch.empty((M, 2), dtype=torch.float32, device=dev)
             st["counts"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
             st["loss"] = torch.empty(1, dtype=torch.float32, device=dev)
             st["d_logits"] = torch.empty_like(st["logits"])
@@ -235,9 +235,9 @@ def _router_own(c, s):
     if not c["train"]:
         X.exl3_router_forward(s["logits"], s["ids"], s["rw"], renorm=c["renorm"])
         return {"ids": s["ids"], "rw": s["rw"]}
-    X.exl3_router_forward(s["logits"], s["ids"], s["rw"], renorm=c["renorm"], lse=s["lse"],
+    X.exl3_router_forward(s["logits"], s["ids"], s["rw"], renorm=c["renorm"], stats=s["stats"],
                           valid=s["valid"], counts=s["counts"], loss=s["loss"], workspace=s["ws"])
-    X.exl3_router_backward(s["logits"], s["ids"], s["lse"], s["d_logits"], renorm=c["renorm"],
+    X.exl3_router_backward(s["logits"], s["ids"], s["stats"], s["d_logits"], renorm=c["renorm"],
                            d_rw=s["d_rw"], valid=s["valid"], counts=s["counts"], d_loss=s["d_loss"])
     return {"ids": s["ids"], "rw": s["rw"], "counts": s["counts"], "loss": s["loss"],
             "d_logits": s["d_logits"]}
