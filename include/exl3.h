@@ -67,6 +67,10 @@ extern "C" {
 
 /* Largest expert count a call accepts. */
 #define EXL3_MAX_EXPERTS 1024
+/* Largest topk of the router, adapter count and adapter rank. */
+#define EXL3_ROUTER_MAX_TOPK 32
+#define EXL3_MAX_ADAPTERS 1024
+#define EXL3_MAX_RANK 128
 
 enum exl3_status {
     EXL3_OK = 0,
@@ -85,7 +89,8 @@ enum exl3_status {
 enum exl3_device_error {
     EXL3_DERR_ROUTE_ID = 1,   /* a route id outside [0, E) */
     EXL3_DERR_TABLE = 2,      /* a used expert / stage table entry is invalid */
-    EXL3_DERR_TIMEOUT = 4     /* a bounded wait on an asynchronous copy gave up */
+    EXL3_DERR_TIMEOUT = 4,    /* a bounded wait on an asynchronous copy gave up */
+    EXL3_DERR_PLAN = 8        /* an adapter plan made for another M or N, or never made */
 };
 
 enum exl3_dtype { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_F32 = 2, EXL3_I32 = 3, EXL3_I64 = 4 };
@@ -223,6 +228,109 @@ int exl3_linear_noalloc(const void *x, int act_dtype, int M, const exl3_proj *pr
  * the current device left in the scratch.  Synchronises; never call it while
  * the stream is capturing.  Returns EXL3_E_NULL for a null err_host. */
 int exl3_linear_noalloc_error(int32_t *err_host, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- router
+ * The step before exl3_moe_forward: logits -> experts and route weights, and
+ * in training the balance loss and the gradient of the logits.
+ *
+ * Per row t: m_t = max_e l_te, s_t = sum_e exp(l_te - m_t), p_te =
+ * exp(l_te - m_t) / s_t.  S_t = the
+ * topk largest logits, descending, ties to the lower expert (-0 equals +0, a
+ * NaN orders below -inf).  rw_tj = p at S_tj, or (renorm) that divided by the
+ * sum of p over S_t.  An expert of logit -inf has p = 0; a row of -inf only has
+ * p = 0, rw = 0 and S = 0..topk-1; a row that holds a NaN or +inf has NaN
+ * weights (its ids are still in [0, E)).
+ * Balance: with valid[t] = 0 for padding rows (NULL: none), c_e = number of
+ * (t, j) of valid rows with S_tj = e, T = number of valid rows and P_e = mean
+ * of p_te over valid rows, loss = E / (topk * T) * sum_e c_e P_e (1 when both
+ * are uniform; 0 when T = 0).  Padding rows are routed like any other. */
+
+/* Bytes of workspace exl3_router_forward needs when it computes the balance. */
+size_t exl3_router_workspace_bytes(int M, int E);
+
+/* logits: [M][E] f16/bf16/f32; ids: int32 [M][topk]; rw: [M][topk] f16/bf16/f32;
+ *   stats: f32 [M][2] = (m_t, s_t), (0, 0) for a row of -inf only, or NULL (the
+ *   backward pass needs it; a sum log s_t + m_t would lose s_t for large m_t).
+ *   counts: int32 [E+1] = c_0..c_{E-1}, T; loss: f32 [1]: both or neither.
+ *   valid: u8 [M] or NULL.  workspace: only with counts (else NULL, 0).
+ *   Sums run in a fixed order: the same call gives the same bits. */
+int exl3_router_forward(const void *logits, int logits_dtype, int M, int E, int topk, int renorm,
+                        int32_t *ids, void *rw, int rw_dtype, float *stats, const uint8_t *valid,
+                        int32_t *counts, float *loss, void *workspace, size_t ws_bytes,
+                        cudaStream_t stream);
+
+/* The gradient of the logits, from ids, stats and counts of the forward pass:
+ *   d_rw: [M][topk] rw_dtype, gradient of rw (NULL: none); d_loss: f32 [1] on
+ *   the device, gradient of loss (with counts; both NULL: none).  Counts are
+ *   constants of the loss; the gradient goes through P.  At least one of d_rw
+ *   and d_loss is needed.  d_logits: [M][E] logits_dtype, and may be logits.
+ *   An id outside [0, E) contributes nothing. */
+int exl3_router_backward(const void *logits, int logits_dtype, int M, int E, int topk, int renorm,
+                         const int32_t *ids, const float *stats, const void *d_rw, int rw_dtype,
+                         const uint8_t *valid, const int32_t *counts, const float *d_loss,
+                         void *d_logits, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside one shared projection (such as
+ * exl3_linear, whose output is `base`): with a(t) the adapter of row t,
+ *   h_t = A_a x_t,   y_t = base_t + scale_a * (h_t B_a),
+ * y_t = base_t for rows without an adapter.  Backward:
+ *   dh_t = scale_a * (B_a dy_t),  dx_t = dx_base_t + dh_t A_a,
+ *   dA_a = sum_t dh_t x_t^T,  dB_a = scale_a * sum_t h_t dy_t^T.
+ * Products accumulate in fp32; h and dh are rounded once to the activation
+ * dtype (they are operands of the second product), every output once. */
+
+/* Device tables of N adapters (host struct; the pointer tables hold device
+ * addresses as int64 and retain nothing).  A: [rank][in], B: [rank][out] in the
+ * activation dtype, contiguous, 16-byte aligned.  0 <= rank <= max_rank; an
+ * adapter of rank 0 changes nothing and its pointers are not read.
+ * in_features and out_features are multiples of 128.  Only entries of adapters
+ * that have rows are read (the backward pass reads every rank). */
+typedef struct exl3_adapters {
+    const int64_t *A;         /* [N] */
+    const int64_t *B;         /* [N] */
+    const int32_t *rank;      /* [N] */
+    const float *scale;       /* [N] */
+    int32_t N;
+    int32_t max_rank;         /* 1..EXL3_MAX_RANK */
+    int32_t in_features;
+    int32_t out_features;
+} exl3_adapters;
+
+/* Groups a batch's rows by adapter (stable).  ids: [M] int32/int64, adapter of
+ * each row in [0, N), or -1 for none; any other id sets EXL3_DERR_ROUTE_ID in
+ * the plan's first word (exl3_workspace_error reads it) and the calls that use
+ * the plan zero-fill their outputs.  One plan serves every adapted projection
+ * the batch passes through.  plan: 256-byte aligned. */
+size_t exl3_lora_plan_bytes(int M, int N);
+int exl3_lora_plan(const void *ids, int ids_dtype, int M, int N, void *plan, size_t plan_bytes,
+                   cudaStream_t stream);
+
+/* Columns of the saved activations h for a largest rank: max_rank rounded up
+ * to 16. */
+int exl3_lora_h_cols(int max_rank);
+
+/* Bytes of workspace exl3_lora_forward / exl3_lora_backward need (256-byte
+ * aligned, need not be initialised; its first word is the call's error word). */
+size_t exl3_lora_workspace_bytes(int M, int N, int in_features, int out_features, int max_rank);
+
+/* x: [M][in]; base: [M][out] or NULL (zero), may be y; y: [M][out]; all
+ *   act_dtype (f16/bf16).  h: act_dtype [M][exl3_lora_h_cols(max_rank)] or
+ *   NULL: what the backward pass needs, rows in plan order. */
+int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *ad,
+                      const void *plan, const void *base, void *y, void *h, void *workspace,
+                      size_t ws_bytes, cudaStream_t stream);
+
+/* dy: [M][out]; x, h: of the forward pass.  dx: [M][in] or NULL (not wanted);
+ *   dx_base: [M][in] or NULL (zero), may be dx.  grads: tables like ad's (its
+ *   A and B point at the outputs dA [rank][in] and dB [rank][out]; its rank and
+ *   scale are not read), or NULL: not wanted; every adapter's gradients are
+ *   written, zeros for one without rows.  At least one of dx, grads is needed.
+ *   Sums over rows run in a fixed order: the same call gives the same bits. */
+int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
+                       const exl3_adapters *ad, const void *plan, const void *dx_base, void *dx,
+                       const exl3_adapters *grads, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
 
 /* Benchmark instrumentation: when `events` is non-NULL, the following calls of
  * exl3_moe_forward / exl3_moe_additive on this host thread record the five

@@ -19,7 +19,7 @@ EXL3_F16, EXL3_BF16, EXL3_F32, EXL3_I32, EXL3_I64 = 0, 1, 2, 3, 4
 EXL3_CB_MUL1, EXL3_CB_MCG, EXL3_CB_3INST = 0, 1, 2
 STATUS = {0: "OK", -1: "E_NULL", -2: "E_DEVICE", -3: "E_DTYPE", -4: "E_SHAPE", -5: "E_ALIGN",
           -6: "E_WORKSPACE", -7: "E_ROUTING", -8: "E_CODEBOOK", -9: "E_CUDA"}
-DERR_ROUTE_ID, DERR_TABLE, DERR_TIMEOUT = 1, 2, 4
+DERR_ROUTE_ID, DERR_TABLE, DERR_TIMEOUT, DERR_PLAN = 1, 2, 4, 8
 
 _DTYPE = {torch.float16: EXL3_F16, torch.bfloat16: EXL3_BF16, torch.float32: EXL3_F32,
           torch.int32: EXL3_I32, torch.int64: EXL3_I64}
@@ -49,6 +49,12 @@ class exl3_stages(ctypes.Structure):
                 ("scale", ctypes.c_void_p), ("K", ctypes.c_void_p)]
 
 
+class exl3_adapters(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("N", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() "
@@ -75,13 +81,34 @@ def _load():
     lib.exl3_profile_events.restype = I
     lib.exl3_workspace_error.argtypes = [V, P(ctypes.c_int32), V]
     lib.exl3_workspace_error.restype = I
+    lib.exl3_router_workspace_bytes.argtypes = [I, I]
+    lib.exl3_router_workspace_bytes.restype = Z
+    lib.exl3_router_forward.argtypes = [V, I, I, I, I, I, V, V, I, V, V, V, V, V, Z, V]
+    lib.exl3_router_forward.restype = I
+    lib.exl3_router_backward.argtypes = [V, I, I, I, I, I, V, V, V, I, V, V, V, V, V]
+    lib.exl3_router_backward.restype = I
+    lib.exl3_lora_plan_bytes.argtypes = [I, I]
+    lib.exl3_lora_plan_bytes.restype = Z
+    lib.exl3_lora_plan.argtypes = [V, I, I, I, V, Z, V]
+    lib.exl3_lora_plan.restype = I
+    lib.exl3_lora_h_cols.argtypes = [I]
+    lib.exl3_lora_h_cols.restype = I
+    lib.exl3_lora_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.exl3_lora_workspace_bytes.restype = Z
+    lib.exl3_lora_forward.argtypes = [V, I, I, V, V, V, V, V, V, Z, V]
+    lib.exl3_lora_forward.restype = I
+    lib.exl3_lora_backward.argtypes = [V, V, V, I, I, V, V, V, V, V, V, Z, V]
+    lib.exl3_lora_backward.restype = I
     return lib
 
 
 _lib = _load()
 EXPORTED = ["exl3_abi_version", "exl3_moe_workspace_bytes", "exl3_linear_workspace_bytes",
             "exl3_route_pack_max_tiles", "exl3_route_pack", "exl3_linear", "exl3_moe_forward",
-            "exl3_moe_additive", "exl3_profile_events", "exl3_workspace_error"]
+            "exl3_moe_additive", "exl3_profile_events", "exl3_workspace_error",
+            "exl3_router_workspace_bytes", "exl3_router_forward", "exl3_router_backward",
+            "exl3_lora_plan_bytes", "exl3_lora_plan", "exl3_lora_h_cols", "exl3_lora_workspace_bytes",
+            "exl3_lora_forward", "exl3_lora_backward"]
 
 
 def lib():
@@ -95,6 +122,10 @@ def _stream(stream):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _check(fn, rc, raise_on_error):
@@ -118,6 +149,22 @@ def exl3_linear_workspace_bytes(M, in_features, out_features) -> int:
 
 def exl3_route_pack_max_tiles(M, topk, E, capacity) -> int:
     return _lib.exl3_route_pack_max_tiles(M, topk, E, capacity)
+
+
+def exl3_router_workspace_bytes(M, E) -> int:
+    return _lib.exl3_router_workspace_bytes(M, E)
+
+
+def exl3_lora_plan_bytes(M, N) -> int:
+    return _lib.exl3_lora_plan_bytes(M, N)
+
+
+def exl3_lora_h_cols(max_rank) -> int:
+    return _lib.exl3_lora_h_cols(max_rank)
+
+
+def exl3_lora_workspace_bytes(M, N, in_features, out_features, max_rank) -> int:
+    return _lib.exl3_lora_workspace_bytes(M, N, in_features, out_features, max_rank)
 
 
 # --------------------------------------------------------------------------- device weights
@@ -235,6 +282,38 @@ class DeviceStages:
                            self.t_K.data_ptr())
 
 
+class DeviceAdapters:
+    """The tables of exl3_adapters over N adapters' device tensors: A[i] is
+    [rank][in], B[i] [rank][out], all of one 16-bit dtype; scales[i] multiplies
+    the update.  The same class over gradient tensors is what
+    exl3_lora_backward writes through.  Keeps the tensors alive."""
+
+    def __init__(self, A, B, scales, max_rank=None):
+        self.A, self.B = list(A), list(B)
+        if not self.A or len(self.A) != len(self.B) or len(self.A) != len(scales):
+            raise ValueError("one A, one B and one scale per adapter")
+        self.N, self.dtype, device = len(self.A), self.A[0].dtype, self.A[0].device
+        self.in_features, self.out_features = self.A[0].shape[1], self.B[0].shape[1]
+        for a, b in zip(self.A, self.B):
+            if (a.shape != (b.shape[0], self.in_features) or b.shape[1] != self.out_features or
+                    a.dtype != self.dtype or b.dtype != self.dtype or a.device != device or
+                    b.device != device or not a.is_contiguous() or not b.is_contiguous()):
+                raise ValueError("A must be [rank][in] and B [rank][out], contiguous, of one "
+                                 "dtype and device")
+        self.ranks = [a.shape[0] for a in self.A]
+        self.max_rank = max(1, max(self.ranks)) if max_rank is None else int(max_rank)
+        self.h_cols = exl3_lora_h_cols(self.max_rank)
+        self.t_A = torch.tensor([a.data_ptr() for a in self.A], dtype=torch.int64, device=device)
+        self.t_B = torch.tensor([b.data_ptr() for b in self.B], dtype=torch.int64, device=device)
+        self.t_rank = torch.tensor(self.ranks, dtype=torch.int32, device=device)
+        self.t_scale = torch.tensor(list(scales), dtype=torch.float32, device=device)
+
+    def struct(self) -> exl3_adapters:
+        return exl3_adapters(self.t_A.data_ptr(), self.t_B.data_ptr(), self.t_rank.data_ptr(),
+                             self.t_scale.data_ptr(), self.N, self.max_rank, self.in_features,
+                             self.out_features)
+
+
 # --------------------------------------------------------------------------- entry points
 def exl3_route_pack(ids, E, capacity, offsets, packed, tiles, info, stream=None,
                     raise_on_error=True) -> int:
@@ -275,6 +354,91 @@ def exl3_moe_additive(x, ids, rw, experts: DeviceExperts, stages: DeviceStages, 
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _ptr(out), _stream(stream))
     return _check("exl3_moe_additive", rc, raise_on_error)
+
+
+def _shaped(what, t, shape, dtype=None):
+    if t is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous() or
+                          (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor"
+                         f"{'' if dtype is None else ' of ' + str(dtype)}")
+
+
+def exl3_router_forward(logits, ids, rw, renorm=False, stats=None, valid=None, counts=None, loss=None,
+                        workspace=None, stream=None, raise_on_error=True) -> int:
+    M, E = logits.shape
+    topk = ids.shape[1]
+    _shaped("logits", logits, (M, E))
+    _shaped("ids", ids, (M, topk), torch.int32)
+    _shaped("rw", rw, (M, topk))
+    _shaped("stats", stats, (M, 2), torch.float32)
+    _shaped("valid", valid, (M,), torch.uint8)
+    _shaped("counts", counts, (E + 1,), torch.int32)
+    _shaped("loss", loss, (1,), torch.float32)
+    rc = _lib.exl3_router_forward(_ptr(logits), _DTYPE[logits.dtype], M, E, topk, int(renorm),
+                                  _ptr(ids), _ptr(rw), _DTYPE[rw.dtype], _ptr(stats), _ptr(valid),
+                                  _ptr(counts), _ptr(loss), _ptr(workspace), _bytes(workspace),
+                                  _stream(stream))
+    return _check("exl3_router_forward", rc, raise_on_error)
+
+
+def exl3_router_backward(logits, ids, stats, d_logits, renorm=False, d_rw=None, valid=None,
+                         counts=None, d_loss=None, stream=None, raise_on_error=True) -> int:
+    M, E = logits.shape
+    topk = ids.shape[1]
+    _shaped("logits", logits, (M, E))
+    _shaped("ids", ids, (M, topk), torch.int32)
+    _shaped("stats", stats, (M, 2), torch.float32)
+    _shaped("d_logits", d_logits, (M, E), logits.dtype)
+    _shaped("d_rw", d_rw, (M, topk))
+    _shaped("valid", valid, (M,), torch.uint8)
+    _shaped("counts", counts, (E + 1,), torch.int32)
+    _shaped("d_loss", d_loss, (1,), torch.float32)
+    rw_dtype = EXL3_F32 if d_rw is None else _DTYPE[d_rw.dtype]
+    rc = _lib.exl3_router_backward(_ptr(logits), _DTYPE[logits.dtype], M, E, topk, int(renorm),
+                                   _ptr(ids), _ptr(stats), _ptr(d_rw), rw_dtype, _ptr(valid),
+                                   _ptr(counts), _ptr(d_loss), _ptr(d_logits), _stream(stream))
+    return _check("exl3_router_backward", rc, raise_on_error)
+
+
+def exl3_lora_plan(ids, N, plan, stream=None, raise_on_error=True) -> int:
+    M = ids.shape[0]
+    _shaped("ids", ids, (M,))
+    rc = _lib.exl3_lora_plan(_ptr(ids), _DTYPE[ids.dtype], M, N, _ptr(plan), _bytes(plan),
+                             _stream(stream))
+    return _check("exl3_lora_plan", rc, raise_on_error)
+
+
+def exl3_lora_forward(x, plan, adapters: DeviceAdapters, y, workspace, base=None, h=None,
+                      stream=None, raise_on_error=True) -> int:
+    M, dt = x.shape[0], adapters.dtype
+    _shaped("x", x, (M, adapters.in_features), dt)
+    _shaped("y", y, (M, adapters.out_features), dt)
+    _shaped("base", base, (M, adapters.out_features), dt)
+    _shaped("h", h, (M, adapters.h_cols), dt)
+    st = adapters.struct()
+    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, ctypes.byref(st), _ptr(plan), _ptr(base),
+                                _ptr(y), _ptr(h), _ptr(workspace), _bytes(workspace),
+                                _stream(stream))
+    return _check("exl3_lora_forward", rc, raise_on_error)
+
+
+def exl3_lora_backward(dy, x, h, plan, adapters: DeviceAdapters, grads, workspace, dx=None,
+                       dx_base=None, stream=None, raise_on_error=True) -> int:
+    M, dt = dy.shape[0], adapters.dtype
+    _shaped("dy", dy, (M, adapters.out_features), dt)
+    _shaped("x", x, (M, adapters.in_features), dt)
+    _shaped("h", h, (M, adapters.h_cols), dt)
+    _shaped("dx", dx, (M, adapters.in_features), dt)
+    _shaped("dx_base", dx_base, (M, adapters.in_features), dt)
+    if grads is not None and (grads.ranks != adapters.ranks or grads.dtype != dt):
+        raise ValueError("grads must hold a tensor like A and one like B for every adapter")
+    st = adapters.struct()
+    gs = None if grads is None else grads.struct()
+    rc = _lib.exl3_lora_backward(_ptr(dy), _ptr(x), _ptr(h), _DTYPE[dt], M, ctypes.byref(st),
+                                 _ptr(plan), _ptr(dx_base), _ptr(dx),
+                                 None if gs is None else ctypes.byref(gs), _ptr(workspace),
+                                 _bytes(workspace), _stream(stream))
+    return _check("exl3_lora_backward", rc, raise_on_error)
 
 
 class ProfileEvents:

@@ -6,7 +6,9 @@
 #include <cstring>
 #include <mutex>
 
+#include "host.h"
 #include "kernels.h"
+#include "lora.h"
 
 using namespace exl3;
 
@@ -38,6 +40,10 @@ void prof_mark(int i, cudaStream_t s)
 // that must precede any capture run them.
 thread_local bool g_capturing = false;
 
+}  // namespace
+
+namespace exl3 {
+
 // Device of the stream (must be the current device); lazily sets kernel attributes.
 int setup_device(cudaStream_t s, int *dev_out, int *sms_out)
 {
@@ -67,7 +73,7 @@ int setup_device(cudaStream_t s, int *dev_out, int *sms_out)
             return EXL3_E_CUDA;
         if (route_pack_set_attributes() != cudaSuccess || gemm_gateup_set_attributes() != cudaSuccess ||
             gemm_down_set_attributes() != cudaSuccess || gemm_linear_set_attributes() != cudaSuccess ||
-            tc_set_attributes() != cudaSuccess)
+            tc_set_attributes() != cudaSuccess || lora_set_attributes() != cudaSuccess)
             return EXL3_E_CUDA;
         d.ready = true;
     }
@@ -89,6 +95,10 @@ bool on_device(const void *p, int dev)
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace exl3
+
+namespace {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (the library
 // does not link the driver library itself); looked up once.
