@@ -87,7 +87,7 @@ def _ad(**kw):
     return B.exl3_adapters(*d.values())
 
 
-_WSB = 1 << 20
+_WSB = 1 << 40
 
 
 def _lf(ad=None, **kw):

@@ -43,36 +43,45 @@ int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, 
     return EXL3_OK;
 }
 
-LoraArgs common_args(int act_dtype, int M, const exl3_adapters *ad, const void *plan, void *ws, int sms)
+// One CTA per SM shares a product's work; the workspace knows kLoraCtas of them.
+int product_ctas(int sms) { return sms < kLoraCtas ? sms : kLoraCtas; }
+
+LoraShrinkArgs shrink_args(int act_dtype, int M, const exl3_adapters *ad, const exl3_adapters *grads,
+                           const void *plan, void *ws, const LoraWsLayout &L)
 {
-    LoraArgs a{};
+    LoraShrinkArgs a{};
     a.plan = static_cast<const int32_t *>(plan);
     a.M = M;
     a.N = ad->N;
     a.act_dtype = act_dtype;
     a.max_rank = ad->max_rank;
     a.h_cols = lora_h_cols(ad->max_rank);
-    a.num_sms = sms;
     a.rank = ad->rank;
-    a.scale = ad->scale;
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
+    a.A = ad->A;
+    a.B = ad->B;
+    a.GA = grads ? grads->A : nullptr;
+    a.GB = grads ? grads->B : nullptr;
     a.hdr = static_cast<int32_t *>(ws);
     return a;
 }
 
-LoraCheckArgs table_check(int M, const exl3_adapters *ad, const exl3_adapters *grads, const void *plan, void *ws)
+// The expand that follows shrink `sh`, launched with `ctas` CTAs.
+LoraExpandArgs expand_args(const LoraShrinkArgs &sh, const exl3_adapters *ad, int ctas)
 {
-    LoraCheckArgs c{};
-    c.plan = static_cast<const int32_t *>(plan);
-    c.M = M;
-    c.N = ad->N;
-    c.max_rank = ad->max_rank;
-    c.A = ad->A;
-    c.B = ad->B;
-    c.GA = grads ? grads->A : nullptr;
-    c.GB = grads ? grads->B : nullptr;
-    c.rank = ad->rank;
-    c.hdr = static_cast<int32_t *>(ws);
-    return c;
+    LoraExpandArgs a{};
+    a.plan = sh.plan;
+    a.M = sh.M;
+    a.N = sh.N;
+    a.act_dtype = sh.act_dtype;
+    a.h_cols = sh.h_cols;
+    a.part = sh.part;
+    a.shrink_width = sh.width;
+    a.shrink_ctas = ctas;
+    a.rank = ad->rank;
+    a.scale = ad->scale;
+    a.hdr = sh.hdr;
+    return a;
 }
 
 }  // namespace
@@ -144,21 +153,20 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
     if (M == 0)
         return EXL3_OK;
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
-    if (launch_lora_check(table_check(M, ad, nullptr, plan, ws), stream) != cudaSuccess)
+    const int ctas = product_ctas(sms);
+    LoraShrinkArgs sh = shrink_args(act_dtype, M, ad, nullptr, plan, ws, L);
+    sh.x = x;
+    sh.W = ad->A;
+    sh.width = ad->in_features;
+    LoraExpandArgs ex = expand_args(sh, ad, ctas);
+    ex.h = h;
+    ex.W = ad->B;
+    ex.width = ad->out_features;
+    ex.base = base;
+    ex.y = y;
+    if (launch_lora_shrink(sh, ctas, stream) != cudaSuccess)
         return EXL3_E_CUDA;
-    LoraArgs a = common_args(act_dtype, M, ad, plan, ws, sms);
-    a.h = h ? h : static_cast<uint8_t *>(ws) + L.h;
-    a.x = x;
-    a.W = ad->A;
-    a.width = ad->in_features;
-    if (launch_lora_shrink(a, stream) != cudaSuccess)
-        return EXL3_E_CUDA;
-    a.W = ad->B;
-    a.width = ad->out_features;
-    a.scaled = 1;
-    a.base = base;
-    a.y = y;
-    return launch_lora_expand(a, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
+    return launch_lora_expand(ex, ctas, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }
 
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
@@ -192,45 +200,39 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
     if (M == 0 && !grads)
         return EXL3_OK;
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
-    if (launch_lora_check(table_check(M, ad, grads, plan, ws), stream) != cudaSuccess)
-        return EXL3_E_CUDA;
-    LoraArgs a = common_args(act_dtype, M, ad, plan, ws, sms);
+    const int ctas = product_ctas(sms);
     void *dh = static_cast<uint8_t *>(ws) + L.h;
-    if (M > 0) {
-        a.h = dh;
-        a.x = dy;
-        a.W = ad->B;
-        a.width = ad->out_features;
-        a.scaled = 1;
-        if (launch_lora_shrink(a, stream) != cudaSuccess)
-            return EXL3_E_CUDA;
-    }
-    if (M > 0 && dx) {
-        a.W = ad->A;
-        a.width = ad->in_features;
-        a.scaled = 0;
-        a.base = dx_base;
-        a.y = dx;
-        if (launch_lora_expand(a, stream) != cudaSuccess)
-            return EXL3_E_CUDA;
-    }
-    if (grads) {
-        a.h = dh;
-        a.x = x;
-        a.G = grads->A;
-        a.width = ad->in_features;
-        a.scaled = 0;
-        if (launch_lora_outer(a, stream) != cudaSuccess)
-            return EXL3_E_CUDA;
-        a.h = const_cast<void *>(h);
-        a.x = dy;
-        a.G = grads->B;
-        a.width = ad->out_features;
-        a.scaled = 1;
-        if (launch_lora_outer(a, stream) != cudaSuccess)
-            return EXL3_E_CUDA;
-    }
-    return EXL3_OK;
+    LoraShrinkArgs sh = shrink_args(act_dtype, M, ad, grads, plan, ws, L);
+    sh.x = dy;
+    sh.W = ad->B;
+    sh.width = ad->out_features;
+    LoraExpandArgs ex = expand_args(sh, ad, ctas);
+    ex.scale_h = 1;
+    ex.h = grads ? dh : nullptr;
+    ex.W = ad->A;
+    ex.width = ad->in_features;
+    ex.base = dx_base;
+    ex.y = dx;
+    if (launch_lora_shrink(sh, ctas, stream) != cudaSuccess)
+        return EXL3_E_CUDA;
+    if (M > 0 && launch_lora_expand(ex, ctas, stream) != cudaSuccess)
+        return EXL3_E_CUDA;
+    if (!grads)
+        return EXL3_OK;
+    LoraOuterArgs o{};
+    o.plan = sh.plan;
+    o.M = M;
+    o.N = sh.N;
+    o.act_dtype = act_dtype;
+    o.h_cols = sh.h_cols;
+    o.ctas = ctas;
+    o.rank = ad->rank;
+    o.scale = ad->scale;
+    o.p[0] = {x, dh, grads->A, ad->in_features, 0};
+    o.p[1] = {dy, h, grads->B, ad->out_features, 1};
+    o.part = sh.part;
+    o.hdr = sh.hdr;
+    return launch_lora_outer(o, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }
 
 }  // extern "C"

@@ -26,9 +26,10 @@ enum LoraPlanWord {
 
 // Rows grouped by adapter: slot s holds row perm[s]; adapter a's slots are
 // offsets[a] .. offsets[a+1], those without an adapter offsets[N] .. M.  A
-// tile is (adapter or -1, first slot, rows, 0).
+// tile is (adapter or -1, first slot, rows, 0).  steps[a]: 64-row steps of the
+// adapters before a (the outer product's contraction).
 struct LoraPlanLayout {
-    size_t offsets, perm, tiles, small, total;
+    size_t offsets, perm, tiles, small, steps, total;
 };
 
 EXL3_HD inline LoraPlanLayout lora_plan_layout(int M, int N)
@@ -39,23 +40,45 @@ EXL3_HD inline LoraPlanLayout lora_plan_layout(int M, int N)
     L.perm = o;    o = align_up(o + (size_t)M * 4, 256);
     L.tiles = o;   o = align_up(o + ((size_t)M / kLoraTile + N + 1) * 16, 256);
     L.small = o;   o = align_up(o + ((size_t)M / kLoraSmallTile + N + 1) * 16, 256);
+    L.steps = o;   o = align_up(o + (size_t)(N + 1) * 4, 256);
     L.total = o;
     return L;
 }
 
 EXL3_HD inline int lora_h_cols(int max_rank) { return (max_rank + 15) / 16 * 16; }
 
+// The products share their work out evenly over at most this many CTAs (one
+// per SM); a workspace is sized for it whatever the device.
+constexpr int kLoraCtas = 152;
+constexpr int kLoraK = 64;           // contraction steps of one pipeline stage
+constexpr int kLoraMinStages = 8;    // stages below which a CTA is not worth its share
+
+// `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).
+EXL3_HD inline int lora_share(int total, int ctas, int least)
+{
+    const int per = (total + ctas - 1) / ctas;
+    return per > least ? per : least;
+}
+
+// Workspace: error word, dh, and fp32 partial sums.  A shrink tile t cut by
+// the shares holds one partial [rows][h_cols] per CTA c that has a part of it,
+// at row (first slot of t) + 128 c: parts of one tile are 128 rows apart, and
+// a later tile never has a lower c, so none overlap.  The outer product keeps
+// at most two partials [h_cols][128] per CTA (its first and its last item).
 struct LoraWsLayout {
-    size_t hdr, h, total;
+    size_t hdr, h, part, total;
 };
 
 EXL3_HD inline LoraWsLayout lora_ws_layout(int M, int N, int in_f, int out_f, int max_rank)
 {
     (void)N; (void)in_f; (void)out_f;
     LoraWsLayout L{};
+    const size_t hc = lora_h_cols(max_rank), shrink = (size_t)M + 128 * (size_t)kLoraCtas;
+    const size_t outer = 2 * 128 * (size_t)kLoraCtas;
     size_t o = 0;
-    L.hdr = o; o = align_up(o + kHdrWords * 4, 256);
-    L.h = o;   o = align_up(o + (size_t)M * lora_h_cols(max_rank) * 2, 256);
+    L.hdr = o;  o = align_up(o + kHdrWords * 4, 256);
+    L.h = o;    o = align_up(o + (size_t)M * hc * 2, 256);
+    L.part = o; o = align_up(o + (shrink > outer ? shrink : outer) * hc * 4, 256);
     L.total = o;
     return L;
 }
@@ -66,40 +89,63 @@ struct LoraPlanArgs {
     int32_t *plan;
 };
 
-// One of the three products, over the rows in plan order:
-//   shrink h[s][j] = alpha_a * sum_i x[perm[s]][i] W_a[j][i]
-//   expand y[perm[s]][n] = base[perm[s]][n] + alpha_a * sum_j h[s][j] W_a[j][n]
-//   outer  G_a[j][n] = alpha_a * sum_s h[s][j] x[perm[s]][n]
-// alpha_a is the adapter's scale where `scaled`, else 1.
-struct LoraArgs {
+// shrink: partial sums over the width of h[s][j] = sum_i x[perm[s]][i] W_a[j][i].
+// Its first CTA also checks the tables (those of adapters that have rows; with
+// gradient tables, of every adapter) and writes the call's error word.
+struct LoraShrinkArgs {
     const int32_t *plan;
-    int M, N, act_dtype, max_rank, h_cols, width, scaled, num_sms;
+    int M, N, act_dtype, max_rank, h_cols, width;
+    const void *x;
+    const int64_t *W;
+    const int32_t *rank;
+    float *part;
+    const int64_t *A, *B, *GA, *GB;
+    int32_t *hdr;
+};
+
+// expand: h = h_scale * (sum of shrink's partials), rounded to the activation
+// type (and kept in `h` where asked), then
+//   y[perm[s]][n] = base[perm[s]][n] + y_scale * sum_j h[s][j] W_a[j][n].
+// h_scale / y_scale: the adapter's scale where `scale_h` / not, else 1.
+// y == nullptr: only h.
+struct LoraExpandArgs {
+    const int32_t *plan;
+    int M, N, act_dtype, h_cols, width, scale_h;
+    const float *part;
+    int shrink_width, shrink_ctas;  // the shares that cut shrink's tiles
+    void *h;
     const int64_t *W;
     const int32_t *rank;
     const float *scale;
-    const int64_t *G;
-    const void *x;
-    void *h;
     const void *base;
     void *y;
     int32_t *hdr;
 };
 
-// Table entries of the adapters that have rows (all: of every adapter, and
-// the gradient tables): the call's error word into hdr.
-struct LoraCheckArgs {
+// outer: G_a[j][n] = g_scale * sum_s h[s][j] x[perm[s]][n], two such products
+// (dA and dB) in one launch; g_scale: the adapter's scale where `scaled`.
+struct LoraOuterArgs {
     const int32_t *plan;
-    int M, N, max_rank;
-    const int64_t *A, *B, *GA, *GB;
+    int M, N, act_dtype, h_cols, ctas;
     const int32_t *rank;
+    const float *scale;
+    struct Product {
+        const void *x, *h;
+        const int64_t *G;
+        int width, scaled;
+    } p[2];
+    float *part;
     int32_t *hdr;
 };
 
 cudaError_t lora_set_attributes();
 cudaError_t launch_lora_plan(const LoraPlanArgs &a, int ids_dtype, cudaStream_t s);
-cudaError_t launch_lora_check(const LoraCheckArgs &a, cudaStream_t s);
-cudaError_t launch_lora_shrink(const LoraArgs &a, cudaStream_t s);
-cudaError_t launch_lora_expand(const LoraArgs &a, cudaStream_t s);
-cudaError_t launch_lora_outer(const LoraArgs &a, cudaStream_t s);
+cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s);
+cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
+cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);
+cudaError_t lora_plan_set_attributes();
+cudaError_t lora_shrink_set_attributes();
+cudaError_t lora_expand_set_attributes();
+cudaError_t lora_outer_set_attributes();
 
 }  // namespace exl3

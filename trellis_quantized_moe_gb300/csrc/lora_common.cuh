@@ -1,0 +1,116 @@
+// What the adapters' tensor-core kernels share: descriptors, copies, the even
+// split of a launch's work and the swizzled shared-memory layout.
+//
+// Operand layouts (16-bit elements, 128-byte rows in groups of 8, the 16-byte
+// chunk c of row r stored at chunk c ^ (r % 8), tiles aligned to 1024 bytes):
+//   K-major:  rows are M or N indices, a row holds 64 contraction steps;
+//   MN-major: rows are contraction steps, a row holds 64 M or N indices; the
+//             next 64 of them start `lbo` bytes on, the next 8 steps 1024.
+#pragma once
+#include "common.cuh"
+#include "expert_tc.cuh"
+#include "lora.h"
+
+namespace exl3 {
+namespace lora {
+
+using tc::fence_after;
+using tc::fence_before;
+using tc::mbar_arrive;
+using tc::mma_commit;
+using tc::mma_f16;
+using tc::tmem_ld16_issue;
+using tc::tmem_ld16_wait;
+using tc::wait_bar;
+using tc::warp_wait_bar;
+
+EXL3_DEV void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+EXL3_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+EXL3_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+EXL3_DEV void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One bulk shared -> global copy of the issuing thread's current group.
+EXL3_DEV void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+                 : "memory");
+}
+EXL3_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+EXL3_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+EXL3_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+EXL3_DEV uint32_t swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+
+EXL3_DEV uint64_t desc_k_major(uint32_t addr) { return tc::smem_desc_swz(addr, 1024, 128); }
+EXL3_DEV uint64_t desc_mn_major(uint32_t addr, uint32_t lbo)
+{
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// f32 accumulate, 16-bit A and B, M = 128, N = n; ta / tb: that operand is MN-major
+EXL3_DEV uint32_t idesc(int n, int act_dtype, int ta, int tb)
+{
+    const uint32_t f = act_dtype == EXL3_BF16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) |
+           ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+EXL3_DEV void tmem_alloc(uint32_t *dst, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+EXL3_DEV void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+// Two values rounded to the activation type, lo in the low half.
+EXL3_DEV uint32_t pack2(float lo, float hi, int dtype)
+{
+    if (dtype == EXL3_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+EXL3_DEV float2 unpack2(uint32_t u, int dtype)
+{
+    if (dtype == EXL3_BF16)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
+{
+    return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;
+}
+
+// Ring position over n slots.
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    EXL3_DEV void next(uint32_t n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+}  // namespace lora
+}  // namespace exl3

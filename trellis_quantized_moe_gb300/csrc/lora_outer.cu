@@ -1,0 +1,351 @@
+// Adapters, gradients of the weights: G_a[j][n] = scale * sum_s h[s][j]
+// x[perm[s]][n] over each adapter's rows, for dA (dh, x) and dB (h, dy) in one
+// launch.
+//
+// 2 r products per element of x or dy against 2 bytes: bound by reading both
+// once.  An item is an adapter's 128 columns; its contraction runs over the
+// rows in 64-row stages.  All stages of both products, laid end to end, are
+// shared out evenly over one CTA per SM; an item inside one share is written
+// out at once, one cut by the shares leaves at most two fp32 partials per CTA
+// for the join kernel, which adds them in CTA order (no atomics: the same bits
+// every time).  The rows come in as they lie in memory: both MMA operands are
+// MN-major (x^T gives the 128 accumulator lanes, h the columns), so nothing is
+// transposed.
+#include "lora_common.cuh"
+
+namespace exl3 {
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 288;       // 4 loader warps, 4 epilogue warps, 1 MMA warp
+constexpr int kLag = 4;
+constexpr int kXBytes = 2 * 64 * 128;
+constexpr int kRingBytes = 208 * 1024;
+constexpr int kMaxSlots = 8;
+constexpr int kJoinThreads = 256;
+constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
+
+EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * (64 * 128); }
+EXL3_HD inline int ring_slots(int h_cols)
+{
+    const int n = kRingBytes / stage_bytes(h_cols);
+    return n < kMaxSlots ? n : kMaxSlots;
+}
+
+struct Ctl {
+    uint64_t full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort;
+};
+
+// Where a stage index lies: product p, adapter e, column block n, and the
+// item's stages [first, first + len).
+struct Item {
+    int p, e, n, first, len;
+};
+
+// The adapter whose steps hold step q: the last e with steps[e] <= q.  One
+// warp: 32 probes 32 apart, then 32 in a row (N <= 1024).
+EXL3_DEV int find_adapter(const int32_t *steps, int N, int q)
+{
+    const int lane = threadIdx.x & 31;
+    const int far = lane * 32;
+    const unsigned m = __ballot_sync(0xffffffffu, far < N && steps[far] <= q);
+    const int base = (31 - __clz(m)) * 32, near = base + lane;
+    const unsigned k = __ballot_sync(0xffffffffu, near < N && steps[near] <= q);
+    return base + 31 - __clz(k);
+}
+
+EXL3_DEV Item locate(const LoraOuterArgs &a, const int32_t *steps, int s)
+{
+    Item it;
+    const int all = steps[a.N], n0 = a.p[0].width / 128;
+    it.p = s >= n0 * all;
+    const int base = it.p ? n0 * all : 0, nb = a.p[it.p].width / 128;
+    it.e = find_adapter(steps, a.N, (s - base) / nb);
+    it.len = steps[it.e + 1] - steps[it.e];
+    const int in = s - base - steps[it.e] * nb;
+    it.n = in / it.len;
+    it.first = s - in % it.len;
+    return it;
+}
+
+// The item after it.
+EXL3_DEV void next_item(const LoraOuterArgs &a, const int32_t *steps, Item &it)
+{
+    it.first += it.len;
+    if (++it.n < a.p[it.p].width / 128)
+        return;
+    it.n = 0;
+    do {
+        if (++it.e == a.N) {
+            it.e = 0;
+            it.p++;
+        }
+        it.len = steps[it.e + 1] - steps[it.e];
+    } while (it.len == 0 && it.p < 2);
+}
+
+EXL3_DEV int total_stages(const LoraOuterArgs &a, const int32_t *steps)
+{
+    return steps[a.N] * (a.p[0].width / 128 + a.p[1].width / 128);
+}
+
+EXL3_DEV void store16(void *p, size_t i, int dtype, float v)
+{
+    if (dtype == EXL3_BF16)
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(p)[i] = __float2half_rn(v);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Ctl c;
+    __shared__ Item start;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (a.hdr[kHdrError])
+        return;
+    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
+    const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
+    const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kLoraMinStages);
+    const int begin = blockIdx.x * per, end = min(total, begin + per);
+    if (begin >= end)
+        return;
+    const int sbytes = stage_bytes(a.h_cols), nslots = ring_slots(a.h_cols);
+    volatile int *abort = &c.abort;
+    if (warp == 0) {
+        const Item it = locate(a, steps, begin);
+        if (lane == 0)
+            start = it;
+    }
+    if (tid == 32) {
+        for (int i = 0; i < nslots; i++) {
+            mbar_init(&c.full[i], 128);
+            mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&c.tfull[i], 1);
+            mbar_init(&c.tempty[i], 128);
+        }
+        c.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8)
+        tmem_alloc(&c.tmem, 256);
+    fence_before();
+    __syncthreads();
+    fence_after();
+
+    Item it = start;
+    auto padded_rank = [&](int e) { return max(16, (a.rank[e] + 15) / 16 * 16); };
+    if (warp < 4) {
+        const int ch = tid & 15, r0 = tid >> 4;     // sixteen lanes per 256-byte row of x
+        Ring put, done;
+        int pending = 0;
+        auto finish = [&]() {
+            fence_proxy();
+            mbar_arrive(&c.full[done.slot]);
+            done.next(nslots);
+            pending--;
+        };
+        bool ok = true;
+        int row[8], slot0 = 0, rows = 0, hc = 2;    // rows of the current stage (-1: past the end)
+        const uint8_t *x = nullptr, *h = nullptr;
+        size_t pitch = 0;
+        auto load_rows = [&](int k) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int r = k * kLoraK + r0 + 8 * i;
+                row[i] = r < rows ? perm[slot0 + r] : -1;
+            }
+        };
+        auto enter = [&](int k) {
+            slot0 = offs[it.e];
+            rows = offs[it.e + 1] - slot0;
+            x = static_cast<const uint8_t *>(a.p[it.p].x) + (size_t)it.n * 256 + ch * 16;
+            h = static_cast<const uint8_t *>(a.p[it.p].h);
+            pitch = (size_t)a.p[it.p].width * 2;
+            hc = padded_rank(it.e) / 8;
+            load_rows(k);
+        };
+        int k = begin - it.first;
+        enter(k);
+        for (int s = begin; s < end; s++) {
+            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+                break;
+            const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                cp_async16(dst + (ch >> 3) * (64 * 128) + swz(r0 + 8 * i, ch & 7),
+                           row[i] < 0 ? x : x + (size_t)row[i] * pitch, row[i] >= 0);
+            for (int i = tid; i < 64 * hc; i += 128) {
+                const int r = i / hc, q = i % hc;
+                const bool v = k * kLoraK + r < rows;
+                cp_async16(dst + kXBytes + (q >> 3) * (64 * 128) + swz(r, q & 7),
+                           v ? h + ((size_t)(slot0 + k * kLoraK + r) * a.h_cols + q * 8) * 2 : h, v);
+            }
+            cp_async_commit();
+            put.next(nslots);
+            if (++k == it.len) {
+                next_item(a, steps, it);
+                k = 0;
+                if (s + 1 < end)
+                    enter(0);
+            } else {
+                load_rows(k);
+            }
+            if (++pending > kLag) {
+                cp_async_wait<kLag>();
+                finish();
+            }
+        }
+        cp_async_wait<0>();
+        while (ok && pending)
+            finish();
+    } else if (warp < 8) {
+        const int q = warp & 3, col = 32 * q + lane;
+        Ring t;
+        for (int s = begin; s < end;) {
+            const int stop = min(end, it.first + it.len);
+            const bool whole = it.first >= begin && it.first + it.len <= end;
+            const int rank = a.rank[it.e], width = a.p[it.p].width;
+            const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
+            void *out = rank > 0 ? reinterpret_cast<void *>(a.p[it.p].G[it.e]) : nullptr;
+            float *part = a.part + (2 * (size_t)blockIdx.x + (s > begin)) * 128 * a.h_cols + col;
+            if (!warp_wait_bar(&c.tfull[t.slot], t.phase, abort, a.hdr))
+                break;
+            fence_after();
+            const uint32_t addr = c.tmem + ((uint32_t)(32 * q) << 16) + t.slot * 128;
+            for (int j = 0; j < rank; j += 16) {
+                uint32_t v[16];
+                tmem_ld16_issue(addr + j, v);
+                tmem_ld16_wait(v);
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        if (j + i < rank)
+                            store16(out, (size_t)(j + i) * width + it.n * 128 + col, a.act_dtype,
+                                    alpha * __uint_as_float(v[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        part[(j + i) * 128] = __uint_as_float(v[i]);
+                }
+            }
+            fence_before();
+            mbar_arrive(&c.tempty[t.slot]);
+            t.next(2);
+            s = stop;
+            if (s < end)
+                next_item(a, steps, it);
+        }
+    } else if (lane == 0) {
+        Ring get, t;
+        bool ok = true;
+        for (int s = begin; s < end && ok;) {
+            const int stop = min(end, it.first + it.len);
+            const uint32_t id = idesc(padded_rank(it.e), a.act_dtype, 1, 1);
+            if (!(ok = wait_bar(&c.tempty[t.slot], t.phase ^ 1, abort, a.hdr)))
+                break;
+            fence_after();
+            bool first = true;
+            for (; s < stop; s++) {
+                if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
+                    break;
+                fence_after();
+                const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    mma_f16(c.tmem + t.slot * 128, desc_mn_major(xs + 2048 * i, 64 * 128),
+                            desc_mn_major(xs + kXBytes + 2048 * i, 64 * 128), id, !(first && i == 0));
+                first = false;
+                mma_commit(&c.empty[get.slot]);
+                get.next(nslots);
+            }
+            mma_commit(&c.tfull[t.slot]);
+            t.next(2);
+            if (s < end)
+                next_item(a, steps, it);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    __syncwarp();
+    if (warp == 8)
+        tmem_free(c.tmem, 256);
+}
+
+// Block c < ctas: the item that the boundary between shares c and c + 1 cuts,
+// if c holds the item's first stage.  The other blocks zero the gradients of
+// adapters without rows.
+__global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
+{
+    if (a.hdr[kHdrError])
+        return;
+    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
+    const int32_t *steps = a.plan + L.steps / 4;
+    if ((int)blockIdx.x >= a.ctas) {
+        for (int e = blockIdx.x - a.ctas; e < a.N; e += kZeroBlocks) {
+            if (steps[e] != steps[e + 1] || a.rank[e] == 0)
+                continue;
+            for (int p = 0; p < 2; p++) {
+                uint4 *out = reinterpret_cast<uint4 *>(a.p[p].G[e]);
+                for (size_t i = threadIdx.x; i < (size_t)a.rank[e] * a.p[p].width / 8; i += kJoinThreads)
+                    out[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        return;
+    }
+    const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kLoraMinStages);
+    const int cut = ((int)blockIdx.x + 1) * per;
+    if (cut >= total)
+        return;
+    const Item it = locate(a, steps, cut);
+    const int c0 = it.first / per, c1 = (it.first + it.len - 1) / per;
+    if (it.first == cut || c0 != (int)blockIdx.x)
+        return;
+    const int rank = a.rank[it.e], width = a.p[it.p].width;
+    const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
+    const size_t slot = 128 * (size_t)a.h_cols;
+    for (int i = threadIdx.x; i < rank * 128; i += kJoinThreads) {
+        float v = 0.0f;
+        for (int c = c0; c <= c1; c++)
+            v += a.part[(2 * (size_t)c + (max(it.first, c * per) > c * per)) * slot + i];
+        store16(reinterpret_cast<void *>(a.p[it.p].G[it.e]), (size_t)(i >> 7) * width + it.n * 128 + (i & 127),
+                a.act_dtype, alpha * v);
+    }
+}
+
+}  // namespace
+
+}  // namespace lora
+
+cudaError_t lora_outer_set_attributes()
+{
+    return cudaFuncSetAttribute(lora::k_lora_outer, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                lora::kRingBytes);
+}
+
+cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s)
+{
+    if (a.M > 0)
+        lora::k_lora_outer<<<a.ctas, lora::kThreads, lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s>>>(a);
+    lora::k_lora_join<<<a.ctas + lora::kZeroBlocks, lora::kJoinThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t lora_set_attributes()
+{
+    cudaError_t e = lora_plan_set_attributes();
+    if (e == cudaSuccess)
+        e = lora_shrink_set_attributes();
+    if (e == cudaSuccess)
+        e = lora_expand_set_attributes();
+    return e == cudaSuccess ? lora_outer_set_attributes() : e;
+}
+
+}  // namespace exl3

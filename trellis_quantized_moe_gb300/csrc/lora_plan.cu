@@ -99,6 +99,13 @@ __global__ void __launch_bounds__(kThreads) k_lora_plan(LoraPlanArgs a)
     const int start = scan_exclusive(rows, sums, &total);
     const int t0 = scan_exclusive((rows + kLoraTile - 1) / kLoraTile, sums, &ntiles);
     const int s0 = scan_exclusive((rows + kLoraSmallTile - 1) / kLoraSmallTile, sums, &nsmall);
+    int nsteps;
+    const int k0 = scan_exclusive((rows + kLoraK - 1) / kLoraK, sums, &nsteps);
+    int32_t *step_off = reinterpret_cast<int32_t *>(base + L.steps);
+    if (tid < N)
+        step_off[tid] = k0;
+    if (tid == 0)
+        step_off[N] = nsteps;
     if (tid < N) {
         offsets[tid] = start;
         for (int w = 0; w < kWarps; w++)
@@ -159,7 +166,7 @@ constexpr int kMaxSmem = kWarps * (EXL3_MAX_ADAPTERS + 1) * 4;
 
 }  // namespace
 
-cudaError_t lora_set_attributes()
+cudaError_t lora_plan_set_attributes()
 {
     cudaError_t e = cudaFuncSetAttribute(k_lora_plan<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kMaxSmem);

@@ -1,0 +1,253 @@
+// Adapters, first product: h[s][j] = sum_i x[perm[s]][i] W_a[j][i] over the
+// rows grouped by adapter (x A^T forward, dy B^T backward).
+//
+// 2 r products per element of x (r <= 128) against 2 bytes: the kernel is
+// bound by reading x once, so what counts is bytes in flight on every SM.
+// The tiles' contractions, laid end to end as 64-wide stages, are shared out
+// evenly over one CTA per SM whatever the tile count (a batch of few rows is
+// split over its width, one of many is not); a tile cut by the shares leaves
+// one fp32 partial per CTA, which the expand kernel adds in CTA order.  A stage
+// is 128 rows x 128 bytes of x and the adapter's rank x 128 bytes of W, copied
+// by cp.async (gathered rows: eight lanes per 128-byte row) into a ring; one
+// thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
+// warps drain the accumulator, double-buffered in TMEM.
+#include "lora_common.cuh"
+
+namespace exl3 {
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 288;       // 4 loader warps, 4 epilogue warps, 1 MMA warp
+constexpr int kLag = 4;             // stages a loader thread has in flight
+constexpr int kXBytes = 128 * 128;
+constexpr int kRingBytes = 208 * 1024;
+constexpr int kMaxSlots = 12;
+constexpr int kBufCols = 128;       // TMEM columns per accumulator
+
+EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols * 128 + 1023) / 1024 * 1024; }
+EXL3_HD inline int ring_slots(int h_cols)
+{
+    const int n = kRingBytes / stage_bytes(h_cols);
+    return n < kMaxSlots ? n : kMaxSlots;
+}
+
+struct Ctl {
+    uint64_t full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort;
+};
+
+// CTA 0: the tables of every adapter in use
+__device__ void check_tables(const LoraShrinkArgs &a)
+{
+    int err;
+    if (a.plan[kLpMagic] != kLoraMagic || a.plan[kLpM] != a.M || a.plan[kLpN] != a.N) {
+        err = EXL3_DERR_PLAN;
+    } else {
+        err = a.plan[kLpError];
+        const int32_t *off = a.plan + lora_plan_layout(a.M, a.N).offsets / 4;
+        for (int i = threadIdx.x; i < a.N; i += kThreads) {
+            if (off[i] == off[i + 1] && !a.GA)
+                continue;
+            const int r = a.rank[i];
+            bool bad = r < 0 || r > a.max_rank;
+            if (r > 0) {
+                bad |= !a.A[i] || (a.A[i] & 15) || !a.B[i] || (a.B[i] & 15);
+                if (a.GA)
+                    bad |= !a.GA[i] || (a.GA[i] & 15) || !a.GB[i] || (a.GB[i] & 15);
+            }
+            err |= bad ? EXL3_DERR_TABLE : 0;
+        }
+    }
+    const int table = __syncthreads_or(err & EXL3_DERR_TABLE);
+    if (threadIdx.x == 0)
+        a.hdr[kHdrError] = err | (table ? EXL3_DERR_TABLE : 0);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Ctl c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0)
+        check_tables(a);
+    if (!plan_ok(a.plan, a.M, a.N))
+        return;
+    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
+    const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4);
+    const int32_t *perm = a.plan + L.perm / 4;
+    const int ks = a.width / kLoraK, total = a.plan[kLpActive] * ks;
+    const int per = lora_share(total, gridDim.x, kLoraMinStages);
+    const int begin = blockIdx.x * per, end = min(total, begin + per);
+    if (begin >= end)
+        return;
+    const int sbytes = stage_bytes(a.h_cols), nslots = ring_slots(a.h_cols);
+    volatile int *abort = &c.abort;
+    if (tid == 0) {
+        for (int i = 0; i < nslots; i++) {
+            mbar_init(&c.full[i], 128);
+            mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&c.tfull[i], 1);
+            mbar_init(&c.tempty[i], 128);
+        }
+        c.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8)
+        tmem_alloc(&c.tmem, 2 * kBufCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+
+    // rank of a tile's adapter as every role sees it: 0 for a bad table entry
+    auto tile_rank = [&](int e) {
+        const int r = a.rank[e];
+        const int64_t w = a.W[e];
+        return r < 0 || r > a.max_rank || !w || (w & 15) ? 0 : r;
+    };
+
+    if (warp < 4) {
+        const int c8 = tid & 7, r0 = tid >> 3;
+        size_t off[8];
+        bool in[8];
+        const uint8_t *w = nullptr;
+        int rank = 0, rp = 16;
+        Ring put, done;
+        int pending = 0, s = begin;
+        auto finish = [&]() {                      // the oldest stage in flight has landed
+            fence_proxy();
+            mbar_arrive(&c.full[done.slot]);
+            done.next(nslots);
+            pending--;
+        };
+        int tile = begin / ks, k = begin % ks;
+        bool fresh = true, ok = true;
+        for (; s < end; s++) {
+            if (fresh) {
+                const int4 t = tiles[tile];
+                rank = tile_rank(t.x);
+                rp = max(16, (rank + 15) / 16 * 16);
+                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + c8 * 16;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = r0 + 16 * i;
+                    in[i] = r < t.z;
+                    off[i] = in[i] ? ((size_t)perm[t.y + r] * a.width + c8 * 8) * 2 : 0;
+                }
+                fresh = false;
+            }
+            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+                break;
+            const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
+            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 128;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                cp_async16(dst + swz(r0 + 16 * i, c8), x + off[i], in[i]);
+            for (int i = 0; i < rp / 16; i++) {
+                const int j = r0 + 16 * i;
+                const bool v = j < rank;
+                cp_async16(dst + kXBytes + swz(j, c8),
+                           v ? w + ((size_t)j * a.width + (size_t)k * kLoraK) * 2 : static_cast<const uint8_t *>(a.x), v);
+            }
+            cp_async_commit();
+            put.next(nslots);
+            if (++pending > kLag) {
+                cp_async_wait<kLag>();
+                finish();
+            }
+            if (++k == ks) {
+                k = 0;
+                tile++;
+                fresh = true;
+            }
+        }
+        cp_async_wait<0>();
+        while (ok && pending)
+            finish();
+    } else if (warp < 8) {
+        const int q = warp & 3, row = 32 * q + lane;
+        int tile = begin / ks;
+        Ring t;
+        for (int s = begin; s < end; tile++) {
+            const int4 ti = tiles[tile];
+            const int rp = max(16, (tile_rank(ti.x) + 15) / 16 * 16);
+            if (!warp_wait_bar(&c.tfull[t.slot], t.phase, abort, a.hdr))
+                break;
+            fence_after();
+            float *out = a.part + ((size_t)ti.y + 128 * (size_t)blockIdx.x + row) * a.h_cols;
+            const uint32_t addr = c.tmem + ((uint32_t)(32 * q) << 16) + t.slot * kBufCols;
+            for (int j = 0; j < rp; j += 16) {
+                uint32_t v[16];
+                tmem_ld16_issue(addr + j, v);
+                tmem_ld16_wait(v);
+                if (row < ti.z)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<uint4 *>(out + j + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            fence_before();
+            mbar_arrive(&c.tempty[t.slot]);
+            t.next(2);
+            s = (tile + 1) * ks;
+        }
+    } else if (lane == 0) {
+        int tile = begin / ks, k = begin % ks;
+        Ring get, t;
+        uint32_t id = 0;
+        bool fresh = true, ok = true;
+        for (int s = begin; s < end && ok; s++) {
+            if (fresh) {
+                id = idesc(max(16, (tile_rank(tiles[tile].x) + 15) / 16 * 16), a.act_dtype, 0, 0);
+                if (!(ok = wait_bar(&c.tempty[t.slot], t.phase ^ 1, abort, a.hdr)))
+                    break;
+                fence_after();
+            }
+            if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
+                break;
+            fence_after();
+            const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                mma_f16(c.tmem + t.slot * kBufCols, desc_k_major(xs + 32 * i), desc_k_major(xs + kXBytes + 32 * i), id,
+                        !(fresh && i == 0));
+            mma_commit(&c.empty[get.slot]);
+            get.next(nslots);
+            fresh = false;
+            if (++k == ks || s + 1 == end) {
+                mma_commit(&c.tfull[t.slot]);
+                t.next(2);
+                k = 0;
+                tile++;
+                fresh = true;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    __syncwarp();
+    if (warp == 8)
+        tmem_free(c.tmem, 2 * kBufCols);
+}
+
+}  // namespace
+
+}  // namespace lora
+
+cudaError_t lora_shrink_set_attributes()
+{
+    return cudaFuncSetAttribute(lora::k_lora_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                lora::kRingBytes);
+}
+
+cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s)
+{
+    const int smem = lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols);
+    lora::k_lora_shrink<<<ctas, lora::kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace exl3
