@@ -100,6 +100,35 @@ EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
     return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;
 }
 
+// cp.async.wait_group for a count known at run time (2..4).
+EXL3_DEV void cp_async_wait_n(int n)
+{
+    if (n >= 4)
+        cp_async_wait<4>();
+    else if (n == 3)
+        cp_async_wait<3>();
+    else
+        cp_async_wait<2>();
+}
+
+// Launch that may start while the kernel before it in the stream still runs;
+// the kernel itself waits (grid_dep_wait) before it touches that one's results.
+template <typename Args>
+cudaError_t launch_dependent(void (*kernel)(Args), int grid, int threads, size_t smem, cudaStream_t s, const Args &a)
+{
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // Ring position over n slots.
 struct Ring {
     uint32_t slot = 0, phase = 0;
@@ -110,7 +139,21 @@ struct Ring {
             phase ^= 1;
         }
     }
+    // two at a time (n >= 2), for loader groups that take turns
+    EXL3_DEV void next2(uint32_t n)
+    {
+        slot += 2;
+        if (slot >= n) {
+            slot -= n;
+            phase ^= 1;
+        }
+    }
 };
+
+// Stages a loader group keeps in flight beyond the one it issues, two groups
+// taking turns on a ring of n slots: n >= 2 * lag + 2, so that a group never
+// waits for a slot whose stage only its own later progress would release.
+EXL3_HD inline int loader_lag(int n) { return n >= 10 ? 4 : n >= 8 ? 3 : 2; }
 
 }  // namespace lora
 }  // namespace exl3

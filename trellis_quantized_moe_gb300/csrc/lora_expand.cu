@@ -17,7 +17,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 320;       // 4 loader, 4 epilogue warps, MMA warp, base warp
+constexpr int kThreads = 448;       // 4 W loader, 4 epilogue, MMA, base and 4 join warps
 constexpr int kPitch = 272;         // bytes of a row slot: 256 + 16
 constexpr int kRowSlot = 128 * kPitch;
 constexpr int kTBufs = 4;           // TMEM accumulators of 128 columns
@@ -45,21 +45,50 @@ struct Ctl {
     int abort;
 };
 
-// h of one tile, four columns of one row: the partials in CTA order, scaled,
-// zero from the rank on.
-EXL3_DEV uint2 joined_h(const LoraExpandArgs &a, int slot, int j, int c0, int c1, int rank, float alpha)
+// Joins h of one tile, thread jt of 128: the partials of CTAs c0..c1 in that
+// order, scaled, zero from the rank on, rounded; into shared memory (hs) and,
+// with keep, into a.h.  A thread has four columns of up to eight rows in
+// flight: the partials lie in L2, and one load at a time took longer (r = 128:
+// 40 us a tile) than everything else in the kernel.
+EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, int c1, float alpha, uint8_t *hs,
+                     bool keep, int jt)
 {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *p = a.part + ((size_t)slot + 128 * (size_t)c0) * a.h_cols + j;
-    for (int c = c0; c <= c1; c++, p += 128 * (size_t)a.h_cols) {
-        const float4 u = *reinterpret_cast<const float4 *>(p);
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    constexpr int kU = 8;
+    const int rp = (rank + 15) / 16 * 16;
+    const int lq = rp <= 16 ? 2 : rp <= 32 ? 3 : rp <= 64 ? 4 : 5;   // lanes per row: 2^lq
+    const int j = (jt & ((1 << lq) - 1)) * 4, step = 128 >> lq;
+    if (j >= rp)
+        return;
+    const size_t cta = 128 * (size_t)a.h_cols;
+    for (int r0 = jt >> lq; r0 < t.z; r0 += kU * step) {
+        float4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; u++)
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *p = a.part + (size_t)(t.y + r0) * a.h_cols + j + c0 * cta;
+        for (int c = c0; c <= c1; c++, p += cta) {
+#pragma unroll
+            for (int u = 0; u < kU; u++)
+                if (r0 + u * step < t.z) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p + (size_t)u * step * a.h_cols);
+                    v[u].x += f.x; v[u].y += f.y; v[u].z += f.z; v[u].w += f.w;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            const int r = r0 + u * step;
+            if (r >= t.z)
+                break;
+            const float4 f = v[u];
+            const uint2 o = make_uint2(
+                pack2(j < rank ? f.x * alpha : 0.f, j + 1 < rank ? f.y * alpha : 0.f, a.act_dtype),
+                pack2(j + 2 < rank ? f.z * alpha : 0.f, j + 3 < rank ? f.w * alpha : 0.f, a.act_dtype));
+            if (hs)
+                *reinterpret_cast<uint2 *>(hs + (j >> 6) * (128 * 128) + swz(r, (j & 63) >> 3) + (j & 4) * 2) = o;
+            if (keep)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = o;
+        }
     }
-    v.x = j < rank ? v.x * alpha : 0.f;
-    v.y = j + 1 < rank ? v.y * alpha : 0.f;
-    v.z = j + 2 < rank ? v.z * alpha : 0.f;
-    v.w = j + 3 < rank ? v.w * alpha : 0.f;
-    return make_uint2(pack2(v.x, v.y, a.act_dtype), pack2(v.z, v.w, a.act_dtype));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
@@ -67,12 +96,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Ctl c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (a.hdr[kHdrError]) {
-        if (a.y) {
-            const size_t n = (size_t)a.M * a.width / 8;
-            for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < n; i += (size_t)gridDim.x * kThreads)
-                static_cast<uint4 *>(a.y)[i] = make_uint4(0, 0, 0, 0);
-        }
+    grid_dep_launch();
+    // an error zero-fills y: 128 threads of every CTA, this one the i0-th
+    auto zero_fill = [&](int i0) {
+        const size_t all = a.y && i0 < 128 ? (size_t)a.M * a.width / 8 : 0;
+        for (size_t i = (size_t)blockIdx.x * 128 + i0; i < all; i += (size_t)gridDim.x * 128)
+            static_cast<uint4 *>(a.y)[i] = make_uint4(0, 0, 0, 0);
+    };
+    if (!plan_ok(a.plan, a.M, a.N)) {
+        zero_fill(tid);
         return;
     }
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
@@ -86,8 +118,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     const int nb = a.y ? a.width / 128 : 1;
     const int total = ntiles * nb, per = lora_share(total, gridDim.x, 1);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
-    if (begin >= end)
+    if (begin >= end) {
+        grid_dep_wait();
+        if (a.hdr[kHdrError])
+            zero_fill(tid);
         return;
+    }
     const Geom g = geom(a.h_cols);
     uint8_t *hbuf = smem, *wring = smem + 2 * g.h_bytes, *rows = wring + g.nw * g.w_bytes;
     volatile int *abort = &c.abort;
@@ -115,10 +151,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     __syncthreads();
     fence_after();
 
-    auto tile_rank = [&](const int4 &t) { return t.x < 0 ? 0 : a.rank[t.x]; };
+    // rank of a tile's adapter as every role sees it: 0 for a bad table entry
+    // (the error word, which shrink writes, is not there yet)
+    auto tile_rank = [&](const int4 &t) {
+        if (t.x < 0)
+            return 0;
+        const int r = a.rank[t.x];
+        const int64_t w = a.W[t.x];
+        return r < 0 || r > a.h_cols || !w || (w & 15) ? 0 : r;
+    };
 
-    if (warp < 4) {
-        Ring hb, w, done;
+    if (warp < 4 && a.y) {
+        // W blocks: rp rows of 256 bytes as two halves of 128-byte rows;
+        // sixteen lanes per row
+        const int ch = tid & 15, j0 = tid >> 4;
+        Ring w, done;
         bool ok = true;
         int pending = 0;                           // W blocks in flight
         auto finish = [&]() {                      // the oldest of them has landed
@@ -136,35 +183,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 continue;
             }
             const uint8_t *W = reinterpret_cast<const uint8_t *>(a.W[t.x]);
-            const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
-            // every W block issued so far must reach the MMA thread before the
-            // wait for the h buffer, which the MMAs reading it release
-            cp_async_wait<0>();
-            while (pending)
-                finish();
-            if (a.y && !(ok = wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr)))
-                break;
-            uint8_t *hs = hbuf + hb.slot * g.h_bytes;
-            const int c0 = tile * sks / sper, c1 = ((tile + 1) * sks - 1) / sper;
-            const bool keep = a.h != nullptr && s % nb == 0;
-            const int quads = rp / 4;
-            for (int i = tid; i < t.z * quads; i += 128) {
-                const int r = i / quads, j = i % quads * 4;
-                const uint2 v = joined_h(a, t.y + r, j, c0, c1, rank, alpha);
-                *reinterpret_cast<uint2 *>(hs + (j >> 6) * (128 * 128) + swz(r, (j & 63) >> 3) + (j & 4) * 2) = v;
-                if (keep)
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = v;
-            }
-            if (!a.y) {
-                s = last;
-                continue;
-            }
-            fence_proxy();
-            mbar_arrive(&c.hfull[hb.slot]);
-            hb.next(2);
-            // W blocks: rp rows of 256 bytes as two halves of 128-byte rows;
-            // sixteen lanes per row
-            const int ch = tid & 15, j0 = tid >> 4;
             for (; s < last; s++) {
                 if (!(ok = wait_bar(&c.wempty[w.slot], w.phase ^ 1, abort, a.hdr)))
                     break;
@@ -187,8 +205,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         cp_async_wait<0>();
         while (ok && pending)
             finish();
-    } else if (warp < 8 && a.y) {
+    } else if (warp >= 10) {
+        grid_dep_wait();                           // the partials and the error word
+        const bool bad = a.hdr[kHdrError] != 0;
+        Ring hb;
+        for (int s = begin; s < end;) {
+            const int tile = s / nb, last = min(end, (tile + 1) * nb);
+            const int4 t = tiles[tile];
+            const int rank = tile_rank(t);
+            if (rank > 0) {
+                const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
+                const int c0 = tile * sks / sper, c1 = ((tile + 1) * sks - 1) / sper;
+                if (a.y && !wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
+                    break;
+                if (!bad)
+                    join_h(a, t, rank, c0, c1, alpha, a.y ? hbuf + hb.slot * g.h_bytes : nullptr,
+                           a.h != nullptr && s % nb == 0, tid - 320);
+                if (a.y) {
+                    fence_proxy();
+                    mbar_arrive(&c.hfull[hb.slot]);
+                    hb.next(2);
+                }
+            }
+            s = last;
+        }
+    } else if (warp >= 4 && warp < 8 && a.y) {
         const int q = warp & 3, row = 32 * q + lane;
+        grid_dep_wait();                           // the error word
+        const bool bad = a.hdr[kHdrError] != 0;
         Ring t4, b;
         int prev = -1;
         for (int s = begin; s < end;) {
@@ -239,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     t4.next(kTBufs);
                 }
                 fence_proxy();
-                if (live)
+                if (live && !bad)
                     bulk_s2g(dst + (size_t)(s % nb) * 256, smem_addr(slot), 256);
                 bulk_commit();
                 bulk_wait_read<1>();               // the previous item's row has left its slot
@@ -252,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 break;
         }
         bulk_wait_all();
+        if (bad)
+            zero_fill(tid - 128);
     } else if (warp == 8 && lane == 0 && a.y) {
         Ring hb, w, t4;
         bool ok = true;
@@ -336,8 +382,7 @@ cudaError_t lora_expand_set_attributes()
 
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s)
 {
-    lora::k_lora_expand<<<ctas, lora::kThreads, lora::geom(a.h_cols).total, s>>>(a);
-    return cudaGetLastError();
+    return lora::launch_dependent(lora::k_lora_expand, ctas, lora::kThreads, lora::geom(a.h_cols).total, s, a);
 }
 
 }  // namespace exl3

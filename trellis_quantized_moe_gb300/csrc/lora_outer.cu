@@ -18,12 +18,12 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 288;       // 4 loader warps, 4 epilogue warps, 1 MMA warp
-constexpr int kLag = 4;
+constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
 constexpr int kXBytes = 2 * 64 * 128;
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 8;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 4;       // blocks per cut item
 constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
 
 EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * (64 * 128); }
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     __shared__ Ctl c;
     __shared__ Item start;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (a.hdr[kHdrError])
+    grid_dep_launch();
+    if (!plan_ok(a.plan, a.M, a.N))
         return;
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
@@ -133,26 +134,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8)
+    if (warp == 12)
         tmem_alloc(&c.tmem, 256);
     fence_before();
     __syncthreads();
     fence_after();
 
+    grid_dep_wait();                // dh and the error word come from the kernels before
+    const bool bad = a.hdr[kHdrError] != 0;
     Item it = start;
     auto padded_rank = [&](int e) { return max(16, (a.rank[e] + 15) / 16 * 16); };
-    if (warp < 4) {
-        const int ch = tid & 15, r0 = tid >> 4;     // sixteen lanes per 256-byte row of x
+    if (bad) {
+    } else if (warp < 8) {
+        // group 0 takes the even stages of the share, group 1 the odd ones
+        const int group = warp >> 2, gt = tid & 127;
+        const int ch = gt & 15, r0 = gt >> 4;       // sixteen lanes per 256-byte row of x
+        const int lag = loader_lag(nslots);
         Ring put, done;
+        put.slot = done.slot = group;
         int pending = 0;
         auto finish = [&]() {
             fence_proxy();
             mbar_arrive(&c.full[done.slot]);
-            done.next(nslots);
+            done.next2(nslots);
             pending--;
         };
         bool ok = true;
-        int row[8], slot0 = 0, rows = 0, hc = 2;    // rows of the current stage (-1: past the end)
+        int row[8], slot0 = 0, rows = 0;            // rows of the current stage (-1: past the end)
+        int hq = 0, hr = 0, hrows = 64, hn = 1;     // h: this thread's chunk, row, row step, passes
+        bool hin = true;
         const uint8_t *x = nullptr, *h = nullptr;
         size_t pitch = 0;
         auto load_rows = [&](int k) {
@@ -168,12 +178,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             x = static_cast<const uint8_t *>(a.p[it.p].x) + (size_t)it.n * 256 + ch * 16;
             h = static_cast<const uint8_t *>(a.p[it.p].h);
             pitch = (size_t)a.p[it.p].width * 2;
-            hc = padded_rank(it.e) / 8;
+            // a row of h is rp / 8 chunks, dealt to a power of two of lanes
+            const int hc = padded_rank(it.e) / 8, lanes = hc <= 2 ? 2 : hc <= 4 ? 4 : hc <= 8 ? 8 : 16;
+            hq = gt & (lanes - 1);
+            hin = hq < hc;
+            hrows = 128 / lanes;
+            hr = gt / lanes;
+            hn = lanes / 2;
+            h += ((size_t)(slot0 + hr) * a.h_cols + hq * 8) * 2;
             load_rows(k);
         };
-        int k = begin - it.first;
-        enter(k);
-        for (int s = begin; s < end; s++) {
+        int k = begin - it.first + group;
+        auto settle = [&]() {                       // k past the item's end: into the next ones
+            bool moved = false;
+            while (k >= it.len) {
+                k -= it.len;
+                next_item(a, steps, it);
+                moved = true;
+            }
+            return moved;
+        };
+        if (begin + group < end) {
+            settle();
+            enter(k);
+        }
+        for (int s = begin + group; s < end; s += 2) {
             if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
@@ -181,31 +210,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             for (int i = 0; i < 8; i++)
                 cp_async16(dst + (ch >> 3) * (64 * 128) + swz(r0 + 8 * i, ch & 7),
                            row[i] < 0 ? x : x + (size_t)row[i] * pitch, row[i] >= 0);
-            for (int i = tid; i < 64 * hc; i += 128) {
-                const int r = i / hc, q = i % hc;
-                const bool v = k * kLoraK + r < rows;
-                cp_async16(dst + kXBytes + (q >> 3) * (64 * 128) + swz(r, q & 7),
-                           v ? h + ((size_t)(slot0 + k * kLoraK + r) * a.h_cols + q * 8) * 2 : h, v);
-            }
+            const uint8_t *hk = h + (size_t)k * kLoraK * a.h_cols * 2;
+            if (hin)
+                for (int i = 0; i < hn; i++) {
+                    const int r = hr + i * hrows;
+                    const bool v = k * kLoraK + r < rows;
+                    cp_async16(dst + kXBytes + (hq >> 3) * (64 * 128) + swz(r, hq & 7),
+                               v ? hk + (size_t)i * hrows * a.h_cols * 2 : x, v);
+                }
             cp_async_commit();
-            put.next(nslots);
-            if (++k == it.len) {
-                next_item(a, steps, it);
-                k = 0;
-                if (s + 1 < end)
-                    enter(0);
-            } else {
-                load_rows(k);
+            put.next2(nslots);
+            if (s + 2 < end) {
+                k += 2;
+                if (settle())
+                    enter(k);
+                else
+                    load_rows(k);
             }
-            if (++pending > kLag) {
-                cp_async_wait<kLag>();
+            if (++pending > lag) {
+                cp_async_wait_n(lag);
                 finish();
             }
         }
         cp_async_wait<0>();
         while (ok && pending)
             finish();
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         const int q = warp & 3, col = 32 * q + lane;
         Ring t;
         for (int s = begin; s < end;) {
@@ -275,21 +305,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     __syncthreads();
     fence_after();
     __syncwarp();
-    if (warp == 8)
+    if (warp == 12)
         tmem_free(c.tmem, 256);
 }
 
-// Block c < ctas: the item that the boundary between shares c and c + 1 cuts,
-// if c holds the item's first stage.  The other blocks zero the gradients of
-// adapters without rows.
+// Blocks 4c .. 4c + 3, c < ctas: a quarter each of the item that the boundary
+// between shares c and c + 1 cuts, if c holds the item's first stage.  The
+// other blocks zero the gradients of adapters without rows.
 __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
 {
-    if (a.hdr[kHdrError])
+    if (!plan_ok(a.plan, a.M, a.N))
         return;
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *steps = a.plan + L.steps / 4;
-    if ((int)blockIdx.x >= a.ctas) {
-        for (int e = blockIdx.x - a.ctas; e < a.N; e += kZeroBlocks) {
+    const int share = blockIdx.x / kJoinParts;
+    if (share >= a.ctas) {
+        grid_dep_wait();
+        if (a.hdr[kHdrError])
+            return;
+        for (int e = blockIdx.x - a.ctas * kJoinParts; e < a.N; e += kZeroBlocks) {
             if (steps[e] != steps[e + 1] || a.rank[e] == 0)
                 continue;
             for (int p = 0; p < 2; p++) {
@@ -301,22 +335,41 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
         return;
     }
     const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kLoraMinStages);
-    const int cut = ((int)blockIdx.x + 1) * per;
+    const int cut = (share + 1) * per;
     if (cut >= total)
         return;
     const Item it = locate(a, steps, cut);
     const int c0 = it.first / per, c1 = (it.first + it.len - 1) / per;
-    if (it.first == cut || c0 != (int)blockIdx.x)
+    if (it.first == cut || c0 != share)
         return;
     const int rank = a.rank[it.e], width = a.p[it.p].width;
     const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
     const size_t slot = 128 * (size_t)a.h_cols;
-    for (int i = threadIdx.x; i < rank * 128; i += kJoinThreads) {
-        float v = 0.0f;
-        for (int c = c0; c <= c1; c++)
-            v += a.part[(2 * (size_t)c + (max(it.first, c * per) > c * per)) * slot + i];
-        store16(reinterpret_cast<void *>(a.p[it.p].G[it.e]), (size_t)(i >> 7) * width + it.n * 128 + (i & 127),
-                a.act_dtype, alpha * v);
+    grid_dep_wait();
+    if (a.hdr[kHdrError])
+        return;
+    uint8_t *out = reinterpret_cast<uint8_t *>(a.p[it.p].G[it.e]);
+    // four columns a thread; a row's 128 columns are one warp
+    constexpr int kU = 4, kStep = kJoinParts * kJoinThreads;
+    for (int i0 = (blockIdx.x % kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * 32; i0 += kU * kStep) {
+        float4 v[kU] = {};
+        for (int c = c0; c <= c1; c++) {
+            const float *p = a.part + (2 * (size_t)c + (max(it.first, c * per) > c * per)) * slot;
+#pragma unroll
+            for (int u = 0; u < kU; u++)
+                if (i0 + u * kStep < rank * 32) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p + 4 * (size_t)(i0 + u * kStep));
+                    v[u].x += f.x; v[u].y += f.y; v[u].z += f.z; v[u].w += f.w;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            const int i = i0 + u * kStep;
+            if (i < rank * 32)
+                *reinterpret_cast<uint2 *>(out + ((size_t)(i >> 5) * width + it.n * 128 + (i & 31) * 4) * 2) =
+                    make_uint2(pack2(alpha * v[u].x, alpha * v[u].y, a.act_dtype),
+                               pack2(alpha * v[u].z, alpha * v[u].w, a.act_dtype));
+        }
     }
 }
 
@@ -332,10 +385,15 @@ cudaError_t lora_outer_set_attributes()
 
 cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s)
 {
-    if (a.M > 0)
-        lora::k_lora_outer<<<a.ctas, lora::kThreads, lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s>>>(a);
-    lora::k_lora_join<<<a.ctas + lora::kZeroBlocks, lora::kJoinThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.M > 0) {
+        const cudaError_t e =
+            lora::launch_dependent(lora::k_lora_outer, a.ctas, lora::kThreads,
+                                   lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s, a);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return lora::launch_dependent(lora::k_lora_join, a.ctas * lora::kJoinParts + lora::kZeroBlocks,
+                                  lora::kJoinThreads, 0, s, a);
 }
 
 cudaError_t lora_set_attributes()

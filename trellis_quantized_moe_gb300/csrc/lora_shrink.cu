@@ -8,7 +8,9 @@
 // split over its width, one of many is not); a tile cut by the shares leaves
 // one fp32 partial per CTA, which the expand kernel adds in CTA order.  A stage
 // is 128 rows x 128 bytes of x and the adapter's rank x 128 bytes of W, copied
-// by cp.async (gathered rows: eight lanes per 128-byte row) into a ring; one
+// by cp.async (gathered rows: eight lanes per 128-byte row) into a ring by two
+// groups of loader warps that take turns, since a stage's copies, wait, proxy
+// fence and arrival in one group take longer than its share of HBM time; one
 // thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
 // warps drain the accumulator, double-buffered in TMEM.
 #include "lora_common.cuh"
@@ -18,8 +20,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 288;       // 4 loader warps, 4 epilogue warps, 1 MMA warp
-constexpr int kLag = 4;             // stages a loader thread has in flight
+constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
 constexpr int kXBytes = 128 * 128;
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 12;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Ctl c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_launch();
     if (blockIdx.x == 0)
         check_tables(a);
     if (!plan_ok(a.plan, a.M, a.N))
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8)
+    if (warp == 12)
         tmem_alloc(&c.tmem, 2 * kBufCols);
     fence_before();
     __syncthreads();
@@ -109,28 +111,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         return r < 0 || r > a.max_rank || !w || (w & 15) ? 0 : r;
     };
 
-    if (warp < 4) {
-        const int c8 = tid & 7, r0 = tid >> 3;
+    if (warp < 8) {
+        // group 0 takes the even stages of the share, group 1 the odd ones
+        const int group = warp >> 2, gt = tid & 127, c8 = gt & 7, r0 = gt >> 3;
+        const int lag = loader_lag(nslots);
+        const size_t wstep = (size_t)a.width * 32;             // 16 rows of W
         size_t off[8];
         bool in[8];
         const uint8_t *w = nullptr;
-        int rank = 0, rp = 16;
+        int rank = 0, nw = 1, pending = 0;
         Ring put, done;
-        int pending = 0, s = begin;
+        put.slot = done.slot = group;
         auto finish = [&]() {                      // the oldest stage in flight has landed
             fence_proxy();
             mbar_arrive(&c.full[done.slot]);
-            done.next(nslots);
+            done.next2(nslots);
             pending--;
         };
-        int tile = begin / ks, k = begin % ks;
+        int tile = (begin + group) / ks, k = (begin + group) % ks;
         bool fresh = true, ok = true;
-        for (; s < end; s++) {
+        for (int s = begin + group; s < end; s += 2) {
             if (fresh) {
                 const int4 t = tiles[tile];
                 rank = tile_rank(t.x);
-                rp = max(16, (rank + 15) / 16 * 16);
-                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + c8 * 16;
+                nw = max(1, (rank + 15) / 16);
+                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + (size_t)r0 * a.width * 2 + c8 * 16;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const int r = r0 + 16 * i;
@@ -146,20 +151,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
 #pragma unroll
             for (int i = 0; i < 8; i++)
                 cp_async16(dst + swz(r0 + 16 * i, c8), x + off[i], in[i]);
-            for (int i = 0; i < rp / 16; i++) {
-                const int j = r0 + 16 * i;
-                const bool v = j < rank;
-                cp_async16(dst + kXBytes + swz(j, c8),
-                           v ? w + ((size_t)j * a.width + (size_t)k * kLoraK) * 2 : static_cast<const uint8_t *>(a.x), v);
+            const uint8_t *wk = w + (size_t)k * 128;
+            for (int i = 0; i < nw; i++, wk += wstep) {
+                const bool v = r0 + 16 * i < rank;
+                cp_async16(dst + kXBytes + i * 2048 + swz(r0, c8), v ? wk : static_cast<const uint8_t *>(a.x), v);
             }
             cp_async_commit();
-            put.next(nslots);
-            if (++pending > kLag) {
-                cp_async_wait<kLag>();
+            put.next2(nslots);
+            if (++pending > lag) {
+                cp_async_wait_n(lag);
                 finish();
             }
-            if (++k == ks) {
-                k = 0;
+            k += 2;
+            if (k >= ks) {
+                k -= ks;
                 tile++;
                 fresh = true;
             }
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         cp_async_wait<0>();
         while (ok && pending)
             finish();
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         const int q = warp & 3, row = 32 * q + lane;
         int tile = begin / ks;
         Ring t;
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     __syncthreads();
     fence_after();
     __syncwarp();
-    if (warp == 8)
+    if (warp == 12)
         tmem_free(c.tmem, 2 * kBufCols);
 }
 
