@@ -50,8 +50,11 @@ EXL3_HD inline int lora_h_cols(int max_rank) { return (max_rank + 15) / 16 * 16;
 // The products share their work out evenly over at most this many CTAs (one
 // per SM); a workspace is sized for it whatever the device.
 constexpr int kLoraCtas = 152;
-constexpr int kLoraK = 64;           // contraction steps of one pipeline stage
-constexpr int kLoraMinStages = 8;    // stages below which a CTA is not worth its share
+constexpr int kShrinkK = 128;        // inputs of one shrink stage
+constexpr int kShrinkMin = 4;        // stages below which a CTA is not worth its share
+constexpr int kOuterK = 64;          // rows of one outer stage
+constexpr int kOuterN = 256;         // columns of one outer item
+constexpr int kOuterMin = 4;
 
 // `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).
 EXL3_HD inline int lora_share(int total, int ctas, int least)
@@ -64,7 +67,7 @@ EXL3_HD inline int lora_share(int total, int ctas, int least)
 // the shares holds one partial [rows][h_cols] per CTA c that has a part of it,
 // at row (first slot of t) + 128 c: parts of one tile are 128 rows apart, and
 // a later tile never has a lower c, so none overlap.  The outer product keeps
-// at most two partials [h_cols][128] per CTA (its first and its last item).
+// at most two partials [h_cols][kOuterN] per CTA (its first and its last item).
 struct LoraWsLayout {
     size_t hdr, h, part, total;
 };
@@ -74,7 +77,7 @@ EXL3_HD inline LoraWsLayout lora_ws_layout(int M, int N, int in_f, int out_f, in
     (void)N; (void)in_f; (void)out_f;
     LoraWsLayout L{};
     const size_t hc = lora_h_cols(max_rank), shrink = (size_t)M + 128 * (size_t)kLoraCtas;
-    const size_t outer = 2 * 128 * (size_t)kLoraCtas;
+    const size_t outer = 2 * kOuterN * (size_t)kLoraCtas;
     size_t o = 0;
     L.hdr = o;  o = align_up(o + kHdrWords * 4, 256);
     L.h = o;    o = align_up(o + (size_t)M * hc * 2, 256);

@@ -34,17 +34,6 @@ template <int N>
 EXL3_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 EXL3_DEV void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One bulk shared -> global copy of the issuing thread's current group.
-EXL3_DEV void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-                 : "memory");
-}
-EXL3_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-EXL3_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-EXL3_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 EXL3_DEV uint32_t swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
 EXL3_DEV uint64_t desc_k_major(uint32_t addr) { return tc::smem_desc_swz(addr, 1024, 128); }
@@ -100,15 +89,17 @@ EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
     return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;
 }
 
-// cp.async.wait_group for a count known at run time (2..4).
+// cp.async.wait_group for a count known at run time (1..4).
 EXL3_DEV void cp_async_wait_n(int n)
 {
     if (n >= 4)
         cp_async_wait<4>();
     else if (n == 3)
         cp_async_wait<3>();
-    else
+    else if (n == 2)
         cp_async_wait<2>();
+    else
+        cp_async_wait<1>();
 }
 
 // Launch that may start while the kernel before it in the stream still runs;
@@ -151,9 +142,9 @@ struct Ring {
 };
 
 // Stages a loader group keeps in flight beyond the one it issues, two groups
-// taking turns on a ring of n slots: n >= 2 * lag + 2, so that a group never
-// waits for a slot whose stage only its own later progress would release.
-EXL3_HD inline int loader_lag(int n) { return n >= 10 ? 4 : n >= 8 ? 3 : 2; }
+// taking turns on a ring of n slots: n > 2 * lag, so that a group never waits
+// for a slot whose stage only a later step of its own would hand over.
+EXL3_HD inline int loader_lag(int n) { return n >= 10 ? 4 : n >= 8 ? 3 : n >= 6 ? 2 : 1; }
 
 }  // namespace lora
 }  // namespace exl3

@@ -3,13 +3,16 @@
 // backward), with h = the sum of the shrink kernel's partials.
 //
 // Bound by reading base and writing y once (2 r products per 4 bytes).  An
-// item is a tile of 128 rows x 128 outputs; a CTA takes a contiguous share of
+// item is a tile of 128 rows x NW outputs; a CTA takes a contiguous share of
 // the items, so a tile's h is joined once per CTA and stays in shared memory
-// for its output blocks.  Rows of base arrive, and rows of y leave, as 256-byte
-// bulk copies (one per row: the rows are scattered) into slots of 272-byte
-// rows, a pitch on which a thread per row has no bank conflicts: the epilogue
-// thread that owns a row reads its accumulator from TMEM, adds it to the row
-// in place and sends the row off itself, with no exchange between threads.
+// for its output blocks.  Two groups of loader warps take turns on the items
+// and copy base rows (gathered) and the W block by cp.async; an epilogue
+// thread owns a row, adds its accumulator (TMEM) to the row in place, and the
+// warp then writes its 32 rows out, 256 contiguous bytes at a time.  Row slots
+// have 16 bytes of padding: a thread per row has no bank conflicts.  (One
+// bulk copy per 256-byte row, in and out, took 38 cycles a copy: 5 us an item.)
+// NW = 128 for ranks up to 64, 64 above: the slots of a ring deep enough to
+// keep HBM busy must fit beside two 32 KB buffers of h.
 #include "lora_common.cuh"
 
 namespace exl3 {
@@ -17,30 +20,32 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 448;       // 4 W loader, 4 epilogue, MMA, base and 4 join warps
-constexpr int kPitch = 272;         // bytes of a row slot: 256 + 16
-constexpr int kRowSlot = 128 * kPitch;
-constexpr int kTBufs = 4;           // TMEM accumulators of 128 columns
+constexpr int kThreads = 544;       // 8 loader, 4 epilogue warps, MMA warp, 4 join warps
+constexpr int kTBufs = 4;           // TMEM accumulators
 constexpr int kMaxRing = 4;
 
-// Shared memory by largest rank: two buffers of h, W blocks, row slots.
+// Shared memory by largest rank and item width: two buffers of h, then slots
+// of 128 padded rows and a W block.
 struct Geom {
-    int h_bytes, w_bytes, nw, nrow, total;
+    int h_bytes, pitch, row_bytes, slot_bytes, nslots, total;
 };
+template <int NW>
 EXL3_HD inline Geom geom(int h_cols)
 {
-    Geom g;
+    Geom g{};
     g.h_bytes = (h_cols + 63) / 64 * 128 * 128;
-    g.w_bytes = h_cols * 256;
-    g.nw = h_cols > 64 ? 2 : 3;
-    g.nrow = h_cols > 64 ? 2 : 4;
-    g.total = 2 * g.h_bytes + g.nw * g.w_bytes + g.nrow * kRowSlot;
+    g.pitch = NW * 2 + 16;
+    g.row_bytes = 128 * g.pitch;                       // a multiple of 1024
+    g.slot_bytes = g.row_bytes + h_cols * NW * 2;
+    const int n = (220 * 1024 - 2 * g.h_bytes) / g.slot_bytes;
+    g.nslots = n < kMaxRing ? n : kMaxRing;
+    g.total = 2 * g.h_bytes + g.nslots * g.slot_bytes;
     return g;
 }
+EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
 
 struct Ctl {
-    uint64_t hfull[2], hempty[2], wfull[kMaxRing], wempty[kMaxRing], bfull[kMaxRing], bempty[kMaxRing],
-        tfull[kTBufs], tempty[kTBufs];
+    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
     uint32_t tmem;
     int abort;
 };
@@ -91,6 +96,7 @@ EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, i
     }
 }
 
+template <int NW>
 __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -111,11 +117,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4);
     const int32_t *perm = a.plan + L.perm / 4;
     const int active = a.plan[kLpActive];
-    const int sks = a.shrink_width / kLoraK;
-    const int sper = lora_share(active * sks, a.shrink_ctas, kLoraMinStages);
+    const int sks = a.shrink_width / kShrinkK;
+    const int sper = lora_share(active * sks, a.shrink_ctas, kShrinkMin);
     // rows without an adapter need nothing when y is base already
     const int ntiles = !a.y || a.base == a.y ? active : a.plan[kLpTiles];
-    const int nb = a.y ? a.width / 128 : 1;
+    const int nb = a.y ? a.width / NW : 1;
     const int total = ntiles * nb, per = lora_share(total, gridDim.x, 1);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
     if (begin >= end) {
@@ -124,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             zero_fill(tid);
         return;
     }
-    const Geom g = geom(a.h_cols);
-    uint8_t *hbuf = smem, *wring = smem + 2 * g.h_bytes, *rows = wring + g.nw * g.w_bytes;
+    const Geom g = geom<NW>(a.h_cols);
+    uint8_t *hbuf = smem, *ring = smem + 2 * g.h_bytes;
     volatile int *abort = &c.abort;
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
@@ -133,10 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             mbar_init(&c.hempty[i], 1);
         }
         for (int i = 0; i < kMaxRing; i++) {
-            mbar_init(&c.wfull[i], 128);
-            mbar_init(&c.wempty[i], 1);
-            mbar_init(&c.bfull[i], 1);
-            mbar_init(&c.bempty[i], 128);
+            mbar_init(&c.full[i], 128);
+            mbar_init(&c.empty[i], 128);
         }
         for (int i = 0; i < kTBufs; i++) {
             mbar_init(&c.tfull[i], 1);
@@ -145,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8)
-        tmem_alloc(&c.tmem, 128 * kTBufs);
+    if (warp == 12)
+        tmem_alloc(&c.tmem, NW * kTBufs);
     fence_before();
     __syncthreads();
     fence_after();
@@ -161,51 +165,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         return r < 0 || r > a.h_cols || !w || (w & 15) ? 0 : r;
     };
 
-    if (warp < 4 && a.y) {
-        // W blocks: rp rows of 256 bytes as two halves of 128-byte rows;
-        // sixteen lanes per row
-        const int ch = tid & 15, j0 = tid >> 4;
-        Ring w, done;
+    if (warp < 8 && a.y) {
+        // group 0 takes the even items of the share, group 1 the odd ones
+        constexpr int kLanes = NW / 8, kStep = 128 / kLanes, kN = 128 / kStep;   // lanes per row, rows a pass
+        const int group = warp >> 2, gt = tid & 127, ch = gt % kLanes, r0 = gt / kLanes;
+        Ring put, done;
+        put.slot = done.slot = group;
         bool ok = true;
-        int pending = 0;                           // W blocks in flight
-        auto finish = [&]() {                      // the oldest of them has landed
+        int pending = 0, rank = 0, rp = 0;
+        size_t off[kN];
+        uint32_t in = 0;                           // bit i: row r0 + i kStep is in the tile
+        const uint8_t *W = nullptr;
+        auto finish = [&]() {                      // the oldest item in flight has landed
             fence_proxy();
-            mbar_arrive(&c.wfull[done.slot]);
-            done.next(g.nw);
+            mbar_arrive(&c.full[done.slot]);
+            done.next2(g.nslots);
             pending--;
         };
-        for (int s = begin; s < end && ok;) {
-            const int tile = s / nb, last = min(end, (tile + 1) * nb);
-            const int4 t = tiles[tile];
-            const int rank = tile_rank(t), rp = (rank + 15) / 16 * 16;
-            if (rank == 0) {
-                s = last;
-                continue;
-            }
-            const uint8_t *W = reinterpret_cast<const uint8_t *>(a.W[t.x]);
-            for (; s < last; s++) {
-                if (!(ok = wait_bar(&c.wempty[w.slot], w.phase ^ 1, abort, a.hdr)))
-                    break;
-                const uint32_t dst = smem_addr(wring + w.slot * g.w_bytes) + (ch >> 3) * (rp * 128);
-                const uint8_t *src = W + (size_t)(s % nb) * 256 + ch * 16;
-                for (int j = j0; j < rp; j += 8)
-                    cp_async16(dst + swz(j, ch & 7), j < rank ? src + (size_t)j * a.width * 2 : W, j < rank);
-                cp_async_commit();
-                w.next(g.nw);
-                pending++;
-                if (g.nw == 3 && pending > 2) {
-                    cp_async_wait<2>();
-                    finish();
-                } else if (g.nw == 2 && pending > 1) {
-                    cp_async_wait<1>();
-                    finish();
+        int tile = -1;
+        for (int s = begin + group; s < end; s += 2) {
+            if (s / nb != tile) {
+                tile = s / nb;
+                const int4 t = tiles[tile];
+                rank = tile_rank(t);
+                rp = (rank + 15) / 16 * 16;
+                W = rank ? reinterpret_cast<const uint8_t *>(a.W[t.x]) + ((size_t)r0 * a.width + ch * 8) * 2 : nullptr;
+                in = 0;
+#pragma unroll
+                for (int i = 0; i < kN; i++) {
+                    const int r = r0 + i * kStep;
+                    off[i] = 0;
+                    if (a.base && r < t.z) {
+                        in |= 1u << i;
+                        off[i] = ((size_t)perm[t.y + r] * a.width + ch * 8) * 2;
+                    }
                 }
+            }
+            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+                break;
+            const size_t col = (size_t)(s - tile * nb) * (NW * 2);
+            const uint32_t dst = smem_addr(ring + put.slot * g.slot_bytes), db = dst + r0 * g.pitch + ch * 16;
+            const uint8_t *base = static_cast<const uint8_t *>(a.base) + col;
+#pragma unroll
+            for (int i = 0; i < kN; i++)
+                if (in >> i & 1)
+                    cp_async16(db + i * kStep * g.pitch, base + off[i], true);
+            const uint32_t dw = dst + g.row_bytes + (ch >> 3) * (rp * 128);
+            const uint8_t *w = W + col;
+            for (int j = r0; j < rp; j += kStep, w += (size_t)kStep * a.width * 2)
+                cp_async16(dw + swz(j, ch & 7), j < rank ? w : W, j < rank);
+            cp_async_commit();
+            put.next2(g.nslots);
+            if (++pending > 1) {                   // two groups, four slots: one more in flight each
+                cp_async_wait<1>();
+                finish();
             }
         }
         cp_async_wait<0>();
         while (ok && pending)
             finish();
-    } else if (warp >= 10) {
+    } else if (warp >= 13) {
         grid_dep_wait();                           // the partials and the error word
         const bool bad = a.hdr[kHdrError] != 0;
         Ring hb;
@@ -220,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     break;
                 if (!bad)
                     join_h(a, t, rank, c0, c1, alpha, a.y ? hbuf + hb.slot * g.h_bytes : nullptr,
-                           a.h != nullptr && s % nb == 0, tid - 320);
+                           a.h != nullptr && s % nb == 0, tid - 416);
                 if (a.y) {
                     fence_proxy();
                     mbar_arrive(&c.hfull[hb.slot]);
@@ -229,52 +248,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             }
             s = last;
         }
-    } else if (warp >= 4 && warp < 8 && a.y) {
+    } else if (warp >= 8 && warp < 12 && a.y) {
+        constexpr int kLanes = NW / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
         const int q = warp & 3, row = 32 * q + lane;
         grid_dep_wait();                           // the error word
         const bool bad = a.hdr[kHdrError] != 0;
-        Ring t4, b;
-        int prev = -1;
+        Ring t4, in;
         for (int s = begin; s < end;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
             const int4 t = tiles[tile];
-            const bool live = row < t.z, mma = tile_rank(t) > 0;
+            const bool mma = tile_rank(t) > 0;
             const float alpha = mma && !a.scale_h ? a.scale[t.x] : 1.0f;
-            uint8_t *dst = static_cast<uint8_t *>(a.y) + (live ? (size_t)perm[t.y + row] * a.width * 2 : 0);
+            const size_t off = row < t.z ? (size_t)perm[t.y + row] * a.width * 2 : 0;
+            const int rows = bad ? 0 : min(32, t.z - 32 * q);      // of this warp, to be written
             bool ok = true;
             for (; s < last; s++) {
-                ok = (!mma || wait_bar(&c.tfull[t4.slot], t4.phase, abort, a.hdr)) &&
-                     (!a.base || wait_bar(&c.bfull[b.slot], b.phase, abort, a.hdr));
+                ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr) &&
+                     (!mma || wait_bar(&c.tfull[t4.slot], t4.phase, abort, a.hdr));
                 if (!(ok = __all_sync(0xffffffffu, ok)))
                     break;
                 fence_after();
-                uint8_t *slot = rows + b.slot * kRowSlot + row * kPitch;
-                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * 128;
+                uint8_t *warp_rows = ring + in.slot * g.slot_bytes + 32 * q * g.pitch;
+                uint8_t *mine = warp_rows + lane * g.pitch;
+                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * NW;
+                if (mma || !a.base) {
 #pragma unroll
-                for (int n = 0; n < 128; n += 16) {
-                    uint32_t v[16];
-                    if (mma) {
-                        tmem_ld16_issue(acc + n, v);
-                        tmem_ld16_wait(v);
-                    } else {
+                    for (int n = 0; n < NW; n += 16) {
+                        uint32_t v[16] = {};
+                        if (mma) {
+                            tmem_ld16_issue(acc + n, v);
+                            tmem_ld16_wait(v);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            v[i] = 0;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 8) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (a.base)
-                            u = *reinterpret_cast<const uint4 *>(slot + (n + i) * 2);
-                        uint32_t *pu = reinterpret_cast<uint32_t *>(&u);
-                        if (mma)
+                        for (int i = 0; i < 16; i += 8) {
+                            uint4 u = make_uint4(0, 0, 0, 0);
+                            if (a.base)
+                                u = *reinterpret_cast<const uint4 *>(mine + (n + i) * 2);
+                            uint32_t *pu = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const float2 f = unpack2(pu[e], a.act_dtype);
                                 pu[e] = pack2(fmaf(alpha, __uint_as_float(v[i + 2 * e]), f.x),
                                               fmaf(alpha, __uint_as_float(v[i + 2 * e + 1]), f.y), a.act_dtype);
                             }
-                        *reinterpret_cast<uint4 *>(slot + (n + i) * 2) = u;
+                            *reinterpret_cast<uint4 *>(mine + (n + i) * 2) = u;
+                        }
                     }
                 }
                 if (mma) {
@@ -282,91 +300,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     mbar_arrive(&c.tempty[t4.slot]);
                     t4.next(kTBufs);
                 }
-                fence_proxy();
-                if (live && !bad)
-                    bulk_s2g(dst + (size_t)(s % nb) * 256, smem_addr(slot), 256);
-                bulk_commit();
-                bulk_wait_read<1>();               // the previous item's row has left its slot
-                if (prev >= 0)
-                    mbar_arrive(&c.bempty[prev]);
-                prev = b.slot;
-                b.next(g.nrow);
+                __syncwarp();
+                uint8_t *out = static_cast<uint8_t *>(a.y) + (size_t)(s - tile * nb) * (NW * 2) + lane % kLanes * 16;
+#pragma unroll 8
+                for (int r0 = 0; r0 < 32; r0 += kRows) {
+                    const int r = r0 + lane / kLanes;
+                    const size_t o = __shfl_sync(0xffffffffu, off, r);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(warp_rows + r * g.pitch + lane % kLanes * 16);
+                    if (r < rows)
+                        *reinterpret_cast<uint4 *>(out + o) = u;
+                }
+                mbar_arrive(&c.empty[in.slot]);
+                in.next(g.nslots);
             }
             if (!ok)
                 break;
         }
-        bulk_wait_all();
         if (bad)
-            zero_fill(tid - 128);
-    } else if (warp == 8 && lane == 0 && a.y) {
-        Ring hb, w, t4;
+            zero_fill(tid - 256);
+    } else if (warp == 12 && lane == 0 && a.y) {
+        Ring hb, in, t4;
         bool ok = true;
         for (int s = begin; s < end && ok;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
             const int rank = tile_rank(tiles[tile]), rp = (rank + 15) / 16 * 16;
             if (rank == 0) {
-                s = last;
+                for (; s < last; s++)
+                    in.next(g.nslots);
                 continue;
             }
-            const uint32_t id = idesc(128, a.act_dtype, 0, 1);
+            const uint32_t id = idesc(NW, a.act_dtype, 0, 1);
             if (!(ok = wait_bar(&c.hfull[hb.slot], hb.phase, abort, a.hdr)))
                 break;
             const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
             for (; s < last; s++) {
-                if (!(ok = wait_bar(&c.wfull[w.slot], w.phase, abort, a.hdr) &&
+                if (!(ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr) &&
                            wait_bar(&c.tempty[t4.slot], t4.phase ^ 1, abort, a.hdr)))
                     break;
                 fence_after();
-                const uint32_t ws = smem_addr(wring + w.slot * g.w_bytes);
+                const uint32_t ws = smem_addr(ring + in.slot * g.slot_bytes + g.row_bytes);
                 for (int k = 0; k < rp / 16; k++)
-                    mma_f16(c.tmem + t4.slot * 128, desc_k_major(hs + (k >> 2) * (128 * 128) + (k & 3) * 32),
+                    mma_f16(c.tmem + t4.slot * NW, desc_k_major(hs + (k >> 2) * (128 * 128) + (k & 3) * 32),
                             desc_mn_major(ws + k * 2048, rp * 128), id, k > 0);
-                mma_commit(&c.wempty[w.slot]);
                 mma_commit(&c.tfull[t4.slot]);
-                w.next(g.nw);
+                in.next(g.nslots);
                 t4.next(kTBufs);
             }
             mma_commit(&c.hempty[hb.slot]);
             hb.next(2);
         }
-    } else if (warp == 9 && a.y && a.base) {
-        Ring b;
-        bool ok = true;
-        for (int s = begin; s < end && ok;) {
-            const int tile = s / nb, last = min(end, (tile + 1) * nb);
-            const int4 t = tiles[tile];
-            const uint8_t *src[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = lane + 32 * i;
-                src[i] = r < t.z ? static_cast<const uint8_t *>(a.base) + (size_t)perm[t.y + r] * a.width * 2 : nullptr;
-            }
-            for (; s < last; s++) {
-                if (!(ok = warp_wait_bar(&c.bempty[b.slot], b.phase ^ 1, abort, a.hdr)))
-                    break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&c.bfull[b.slot], t.z * 256);
-                __syncwarp();
-                uint8_t *slot = rows + b.slot * kRowSlot;
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (src[i])
-                        bulk_g2s(slot + (lane + 32 * i) * kPitch, src[i] + (size_t)(s % nb) * 256, 256,
-                                 &c.bfull[b.slot]);
-                b.next(g.nrow);
-            }
-        }
-        // after a timeout elsewhere: copies in flight land before the CTA exits
-        if (!ok || *abort)
-            for (int i = 0; i < g.nrow; i++)
-                mbar_wait(&c.bfull[i], (b.slot > (uint32_t)i ? b.phase : b.phase ^ 1));
     }
     fence_before();
     __syncthreads();
     fence_after();
     __syncwarp();
-    if (warp == 8)
-        tmem_free(c.tmem, 128 * kTBufs);
+    if (warp == 12)
+        tmem_free(c.tmem, NW * kTBufs);
 }
 
 }  // namespace
@@ -375,14 +364,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
 
 cudaError_t lora_expand_set_attributes()
 {
-    const int a = lora::geom(16).total, b = lora::geom(64).total, d = lora::geom(128).total;
-    return cudaFuncSetAttribute(lora::k_lora_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                a > b ? (a > d ? a : d) : (b > d ? b : d));
+    const cudaError_t e = cudaFuncSetAttribute(lora::k_lora_expand<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               220 * 1024);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(lora::k_lora_expand<64>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
 }
 
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s)
 {
-    return lora::launch_dependent(lora::k_lora_expand, ctas, lora::kThreads, lora::geom(a.h_cols).total, s, a);
+    if (lora::narrow(a.h_cols))
+        return lora::launch_dependent(lora::k_lora_expand<64>, ctas, lora::kThreads, lora::geom<64>(a.h_cols).total,
+                                      s, a);
+    return lora::launch_dependent(lora::k_lora_expand<128>, ctas, lora::kThreads, lora::geom<128>(a.h_cols).total, s,
+                                  a);
 }
 
 }  // namespace exl3

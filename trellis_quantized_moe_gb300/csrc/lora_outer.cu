@@ -3,7 +3,8 @@
 // launch.
 //
 // 2 r products per element of x or dy against 2 bytes: bound by reading both
-// once.  An item is an adapter's 128 columns; its contraction runs over the
+// once.  An item is an adapter's 256 columns (two accumulators of 128 lanes,
+// so that h is fetched half as often); its contraction runs over the
 // rows in 64-row stages.  All stages of both products, laid end to end, are
 // shared out evenly over one CTA per SM; an item inside one share is written
 // out at once, one cut by the shares leaves at most two fp32 partials per CTA
@@ -19,14 +20,16 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
-constexpr int kXBytes = 2 * 64 * 128;
+constexpr int kBlock = 64 * 128;                 // 64 rows of 64 columns
+constexpr int kXBytes = kOuterN / 64 * kBlock;
+constexpr int kHalfCols = 128;                   // TMEM columns of one 128-column half
 constexpr int kRingBytes = 208 * 1024;
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 6;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 4;       // blocks per cut item
 constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
 
-EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * (64 * 128); }
+EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * kBlock; }
 EXL3_HD inline int ring_slots(int h_cols)
 {
     const int n = kRingBytes / stage_bytes(h_cols);
@@ -38,6 +41,10 @@ struct Ctl {
     uint32_t tmem;
     int abort;
 };
+
+// Items of one adapter: 256 columns, the last one 128 where the width is an
+// odd multiple of 128.
+EXL3_HD inline int blocks(int width) { return (width + kOuterN - 1) / kOuterN; }
 
 // Where a stage index lies: product p, adapter e, column block n, and the
 // item's stages [first, first + len).
@@ -60,9 +67,9 @@ EXL3_DEV int find_adapter(const int32_t *steps, int N, int q)
 EXL3_DEV Item locate(const LoraOuterArgs &a, const int32_t *steps, int s)
 {
     Item it;
-    const int all = steps[a.N], n0 = a.p[0].width / 128;
+    const int all = steps[a.N], n0 = blocks(a.p[0].width);
     it.p = s >= n0 * all;
-    const int base = it.p ? n0 * all : 0, nb = a.p[it.p].width / 128;
+    const int base = it.p ? n0 * all : 0, nb = blocks(a.p[it.p].width);
     it.e = find_adapter(steps, a.N, (s - base) / nb);
     it.len = steps[it.e + 1] - steps[it.e];
     const int in = s - base - steps[it.e] * nb;
@@ -75,7 +82,7 @@ EXL3_DEV Item locate(const LoraOuterArgs &a, const int32_t *steps, int s)
 EXL3_DEV void next_item(const LoraOuterArgs &a, const int32_t *steps, Item &it)
 {
     it.first += it.len;
-    if (++it.n < a.p[it.p].width / 128)
+    if (++it.n < blocks(a.p[it.p].width))
         return;
     it.n = 0;
     do {
@@ -89,7 +96,7 @@ EXL3_DEV void next_item(const LoraOuterArgs &a, const int32_t *steps, Item &it)
 
 EXL3_DEV int total_stages(const LoraOuterArgs &a, const int32_t *steps)
 {
-    return steps[a.N] * (a.p[0].width / 128 + a.p[1].width / 128);
+    return steps[a.N] * (blocks(a.p[0].width) + blocks(a.p[1].width));
 }
 
 EXL3_DEV void store16(void *p, size_t i, int dtype, float v)
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         return;
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
-    const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kLoraMinStages);
+    const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kOuterMin);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
     if (begin >= end)
         return;
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         fence_mbar_init();
     }
     if (warp == 12)
-        tmem_alloc(&c.tmem, 256);
+        tmem_alloc(&c.tmem, 4 * kHalfCols);
     fence_before();
     __syncthreads();
     fence_after();
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     } else if (warp < 8) {
         // group 0 takes the even stages of the share, group 1 the odd ones
         const int group = warp >> 2, gt = tid & 127;
-        const int ch = gt & 15, r0 = gt >> 4;       // sixteen lanes per 256-byte row of x
+        const int ch = gt & 31, r0 = gt >> 5;       // a warp per 512-byte row of x
         const int lag = loader_lag(nslots);
         Ring put, done;
         put.slot = done.slot = group;
@@ -160,22 +167,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             pending--;
         };
         bool ok = true;
-        int row[8], slot0 = 0, rows = 0;            // rows of the current stage (-1: past the end)
+        int row[16], slot0 = 0, rows = 0;            // rows of the current stage (-1: past the end)
         int hq = 0, hr = 0, hrows = 64, hn = 1;     // h: this thread's chunk, row, row step, passes
-        bool hin = true;
+        bool hin = true, xin = true;                 // xin: this thread's chunk is in the item
         const uint8_t *x = nullptr, *h = nullptr;
         size_t pitch = 0;
         auto load_rows = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int r = k * kLoraK + r0 + 8 * i;
-                row[i] = r < rows ? perm[slot0 + r] : -1;
+            for (int i = 0; i < 16; i++) {
+                const int r = k * kOuterK + r0 + 4 * i;
+                row[i] = r < rows && xin ? perm[slot0 + r] : -1;
             }
         };
         auto enter = [&](int k) {
             slot0 = offs[it.e];
             rows = offs[it.e + 1] - slot0;
-            x = static_cast<const uint8_t *>(a.p[it.p].x) + (size_t)it.n * 256 + ch * 16;
+            x = static_cast<const uint8_t *>(a.p[it.p].x) + (size_t)it.n * (2 * kOuterN) + ch * 16;
+            xin = it.n * kOuterN + ch * 8 < a.p[it.p].width;
             h = static_cast<const uint8_t *>(a.p[it.p].h);
             pitch = (size_t)a.p[it.p].width * 2;
             // a row of h is rp / 8 chunks, dealt to a power of two of lanes
@@ -207,16 +215,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                cp_async16(dst + (ch >> 3) * (64 * 128) + swz(r0 + 8 * i, ch & 7),
-                           row[i] < 0 ? x : x + (size_t)row[i] * pitch, row[i] >= 0);
-            const uint8_t *hk = h + (size_t)k * kLoraK * a.h_cols * 2;
+            for (int i = 0; i < 16; i++)
+                cp_async16(dst + (ch >> 3) * kBlock + swz(r0 + 4 * i, ch & 7),
+                           row[i] < 0 ? static_cast<const uint8_t *>(a.p[0].x) : x + (size_t)row[i] * pitch, row[i] >= 0);
+            const uint8_t *hk = h + (size_t)k * kOuterK * a.h_cols * 2;
             if (hin)
                 for (int i = 0; i < hn; i++) {
                     const int r = hr + i * hrows;
-                    const bool v = k * kLoraK + r < rows;
-                    cp_async16(dst + kXBytes + (hq >> 3) * (64 * 128) + swz(r, hq & 7),
-                               v ? hk + (size_t)i * hrows * a.h_cols * 2 : x, v);
+                    const bool v = k * kOuterK + r < rows;
+                    cp_async16(dst + kXBytes + (hq >> 3) * kBlock + swz(r, hq & 7),
+                               v ? hk + (size_t)i * hrows * a.h_cols * 2 : static_cast<const uint8_t *>(a.p[0].x), v);
                 }
             cp_async_commit();
             put.next2(nslots);
@@ -244,25 +252,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             const int rank = a.rank[it.e], width = a.p[it.p].width;
             const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
             void *out = rank > 0 ? reinterpret_cast<void *>(a.p[it.p].G[it.e]) : nullptr;
-            float *part = a.part + (2 * (size_t)blockIdx.x + (s > begin)) * 128 * a.h_cols + col;
+            float *part = a.part + (2 * (size_t)blockIdx.x + (s > begin)) * kOuterN * a.h_cols + col;
             if (!warp_wait_bar(&c.tfull[t.slot], t.phase, abort, a.hdr))
                 break;
             fence_after();
-            const uint32_t addr = c.tmem + ((uint32_t)(32 * q) << 16) + t.slot * 128;
-            for (int j = 0; j < rank; j += 16) {
-                uint32_t v[16];
-                tmem_ld16_issue(addr + j, v);
-                tmem_ld16_wait(v);
-                if (whole) {
+            const int halves = min(2, (width - it.n * kOuterN) / 128);
+            for (int half = 0; half < halves; half++) {
+                const uint32_t addr = c.tmem + ((uint32_t)(32 * q) << 16) + (2 * t.slot + half) * kHalfCols;
+                for (int j = 0; j < rank; j += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_issue(addr + j, v);
+                    tmem_ld16_wait(v);
+                    if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        if (j + i < rank)
-                            store16(out, (size_t)(j + i) * width + it.n * 128 + col, a.act_dtype,
-                                    alpha * __uint_as_float(v[i]));
-                } else {
+                        for (int i = 0; i < 16; i++)
+                            if (j + i < rank)
+                                store16(out, (size_t)(j + i) * width + it.n * kOuterN + half * 128 + col,
+                                        a.act_dtype, alpha * __uint_as_float(v[i]));
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        part[(j + i) * 128] = __uint_as_float(v[i]);
+                        for (int i = 0; i < 16; i++)
+                            part[(j + i) * kOuterN + half * 128] = __uint_as_float(v[i]);
+                    }
                 }
             }
             fence_before();
@@ -281,16 +292,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             if (!(ok = wait_bar(&c.tempty[t.slot], t.phase ^ 1, abort, a.hdr)))
                 break;
             fence_after();
+            const int halves = min(2, (a.p[it.p].width - it.n * kOuterN) / 128);
             bool first = true;
             for (; s < stop; s++) {
                 if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
                     break;
                 fence_after();
                 const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
+                for (int half = 0; half < halves; half++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    mma_f16(c.tmem + t.slot * 128, desc_mn_major(xs + 2048 * i, 64 * 128),
-                            desc_mn_major(xs + kXBytes + 2048 * i, 64 * 128), id, !(first && i == 0));
+                    for (int i = 0; i < 4; i++)
+                        mma_f16(c.tmem + (2 * t.slot + half) * kHalfCols,
+                                desc_mn_major(xs + half * 2 * kBlock + 2048 * i, kBlock),
+                                desc_mn_major(xs + kXBytes + 2048 * i, kBlock), id, !(first && i == 0));
                 first = false;
                 mma_commit(&c.empty[get.slot]);
                 get.next(nslots);
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     fence_after();
     __syncwarp();
     if (warp == 12)
-        tmem_free(c.tmem, 256);
+        tmem_free(c.tmem, 4 * kHalfCols);
 }
 
 // Blocks 4c .. 4c + 3, c < ctas: a quarter each of the item that the boundary
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
         }
         return;
     }
-    const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kLoraMinStages);
+    const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kOuterMin);
     const int cut = (share + 1) * per;
     if (cut >= total)
         return;
@@ -344,29 +358,31 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
         return;
     const int rank = a.rank[it.e], width = a.p[it.p].width;
     const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
-    const size_t slot = 128 * (size_t)a.h_cols;
+    const size_t slot = kOuterN * (size_t)a.h_cols;
+    const int quads = min(kOuterN, width - it.n * kOuterN) / 4;    // 64 or 32 a row
     grid_dep_wait();
     if (a.hdr[kHdrError])
         return;
     uint8_t *out = reinterpret_cast<uint8_t *>(a.p[it.p].G[it.e]);
-    // four columns a thread; a row's 128 columns are one warp
+    // four columns a thread
     constexpr int kU = 4, kStep = kJoinParts * kJoinThreads;
-    for (int i0 = (blockIdx.x % kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * 32; i0 += kU * kStep) {
+    for (int i0 = (blockIdx.x % kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * quads; i0 += kU * kStep) {
         float4 v[kU] = {};
         for (int c = c0; c <= c1; c++) {
             const float *p = a.part + (2 * (size_t)c + (max(it.first, c * per) > c * per)) * slot;
 #pragma unroll
             for (int u = 0; u < kU; u++)
-                if (i0 + u * kStep < rank * 32) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p + 4 * (size_t)(i0 + u * kStep));
+                if (i0 + u * kStep < rank * quads) {
+                    const int i = i0 + u * kStep;
+                    const float4 f = *reinterpret_cast<const float4 *>(p + i / quads * kOuterN + i % quads * 4);
                     v[u].x += f.x; v[u].y += f.y; v[u].z += f.z; v[u].w += f.w;
                 }
         }
 #pragma unroll
         for (int u = 0; u < kU; u++) {
             const int i = i0 + u * kStep;
-            if (i < rank * 32)
-                *reinterpret_cast<uint2 *>(out + ((size_t)(i >> 5) * width + it.n * 128 + (i & 31) * 4) * 2) =
+            if (i < rank * quads)
+                *reinterpret_cast<uint2 *>(out + ((size_t)(i / quads) * width + it.n * kOuterN + i % quads * 4) * 2) =
                     make_uint2(pack2(alpha * v[u].x, alpha * v[u].y, a.act_dtype),
                                pack2(alpha * v[u].z, alpha * v[u].w, a.act_dtype));
         }

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_plan(LoraPlanArgs a)
     const int t0 = scan_exclusive((rows + kLoraTile - 1) / kLoraTile, sums, &ntiles);
     const int s0 = scan_exclusive((rows + kLoraSmallTile - 1) / kLoraSmallTile, sums, &nsmall);
     int nsteps;
-    const int k0 = scan_exclusive((rows + kLoraK - 1) / kLoraK, sums, &nsteps);
+    const int k0 = scan_exclusive((rows + kOuterK - 1) / kOuterK, sums, &nsteps);
     int32_t *step_off = reinterpret_cast<int32_t *>(base + L.steps);
     if (tid < N)
         step_off[tid] = k0;

@@ -3,12 +3,12 @@
 //
 // 2 r products per element of x (r <= 128) against 2 bytes: the kernel is
 // bound by reading x once, so what counts is bytes in flight on every SM.
-// The tiles' contractions, laid end to end as 64-wide stages, are shared out
+// The tiles' contractions, laid end to end as 128-wide stages, are shared out
 // evenly over one CTA per SM whatever the tile count (a batch of few rows is
 // split over its width, one of many is not); a tile cut by the shares leaves
 // one fp32 partial per CTA, which the expand kernel adds in CTA order.  A stage
-// is 128 rows x 128 bytes of x and the adapter's rank x 128 bytes of W, copied
-// by cp.async (gathered rows: eight lanes per 128-byte row) into a ring by two
+// is 128 rows x 256 bytes of x and the adapter's rank x 256 bytes of W, copied
+// by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring by two
 // groups of loader warps that take turns, since a stage's copies, wait, proxy
 // fence and arrival in one group take longer than its share of HBM time; one
 // thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
@@ -21,12 +21,12 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
-constexpr int kXBytes = 128 * 128;
+constexpr int kXBytes = 2 * 128 * 128;   // two 64-wide blocks
 constexpr int kRingBytes = 208 * 1024;
-constexpr int kMaxSlots = 12;
+constexpr int kMaxSlots = 6;
 constexpr int kBufCols = 128;       // TMEM columns per accumulator
 
-EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols * 128 + 1023) / 1024 * 1024; }
+EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + h_cols * 256; }
 EXL3_HD inline int ring_slots(int h_cols)
 {
     const int n = kRingBytes / stage_bytes(h_cols);
@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4);
     const int32_t *perm = a.plan + L.perm / 4;
-    const int ks = a.width / kLoraK, total = a.plan[kLpActive] * ks;
-    const int per = lora_share(total, gridDim.x, kLoraMinStages);
+    const int ks = a.width / kShrinkK, total = a.plan[kLpActive] * ks;
+    const int per = lora_share(total, gridDim.x, kShrinkMin);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
     if (begin >= end)
         return;
@@ -113,13 +113,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
 
     if (warp < 8) {
         // group 0 takes the even stages of the share, group 1 the odd ones
-        const int group = warp >> 2, gt = tid & 127, c8 = gt & 7, r0 = gt >> 3;
+        const int group = warp >> 2, gt = tid & 127, ch = gt & 15, r0 = gt >> 4;
         const int lag = loader_lag(nslots);
-        const size_t wstep = (size_t)a.width * 32;             // 16 rows of W
-        size_t off[8];
-        bool in[8];
+        const size_t wstep = (size_t)a.width * 16;             // 8 rows of W
+        size_t off[16];
+        uint32_t in = 0;                           // bit i: row r0 + 8 i is in the tile
         const uint8_t *w = nullptr;
-        int rank = 0, nw = 1, pending = 0;
+        int rank = 0, rp = 16, pending = 0;
         Ring put, done;
         put.slot = done.slot = group;
         auto finish = [&]() {                      // the oldest stage in flight has landed
@@ -134,27 +134,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             if (fresh) {
                 const int4 t = tiles[tile];
                 rank = tile_rank(t.x);
-                nw = max(1, (rank + 15) / 16);
-                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + (size_t)r0 * a.width * 2 + c8 * 16;
+                rp = max(16, (rank + 15) / 16 * 16);
+                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + (size_t)r0 * a.width * 2 + ch * 16;
+                in = 0;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int r = r0 + 16 * i;
-                    in[i] = r < t.z;
-                    off[i] = in[i] ? ((size_t)perm[t.y + r] * a.width + c8 * 8) * 2 : 0;
+                for (int i = 0; i < 16; i++) {
+                    const int r = r0 + 8 * i;
+                    in |= (uint32_t)(r < t.z) << i;
+                    off[i] = r < t.z ? ((size_t)perm[t.y + r] * a.width + ch * 8) * 2 : 0;
                 }
                 fresh = false;
             }
             if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
-            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 128;
+            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 256;
+            // 64-wide block ch / 8, row r0 + 8 i, chunk ch % 8
+            const uint32_t dx = dst + (ch >> 3) * (128 * 128) + swz(r0, ch & 7);
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                cp_async16(dst + swz(r0 + 16 * i, c8), x + off[i], in[i]);
-            const uint8_t *wk = w + (size_t)k * 128;
-            for (int i = 0; i < nw; i++, wk += wstep) {
-                const bool v = r0 + 16 * i < rank;
-                cp_async16(dst + kXBytes + i * 2048 + swz(r0, c8), v ? wk : static_cast<const uint8_t *>(a.x), v);
+            for (int i = 0; i < 16; i++)
+                cp_async16(dx + i * 1024, x + off[i], in >> i & 1);
+            const uint8_t *wk = w + (size_t)k * 256;
+            const uint32_t dw = dst + kXBytes + (ch >> 3) * (rp * 128) + swz(r0, ch & 7);
+            for (int i = 0; i < rp / 8; i++, wk += wstep) {
+                const bool v = r0 + 8 * i < rank;
+                cp_async16(dw + i * 1024, v ? wk : static_cast<const uint8_t *>(a.x), v);
             }
             cp_async_commit();
             put.next2(nslots);
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 finish();
             }
             k += 2;
-            if (k >= ks) {
+            while (k >= ks) {                      // ks may be 1
                 k -= ks;
                 tile++;
                 fresh = true;
@@ -202,10 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         int tile = begin / ks, k = begin % ks;
         Ring get, t;
         uint32_t id = 0;
+        int rp = 16;
         bool fresh = true, ok = true;
         for (int s = begin; s < end && ok; s++) {
             if (fresh) {
-                id = idesc(max(16, (tile_rank(tiles[tile].x) + 15) / 16 * 16), a.act_dtype, 0, 0);
+                rp = max(16, (tile_rank(tiles[tile].x) + 15) / 16 * 16);
+                id = idesc(rp, a.act_dtype, 0, 0);
                 if (!(ok = wait_bar(&c.tempty[t.slot], t.phase ^ 1, abort, a.hdr)))
                     break;
                 fence_after();
@@ -215,9 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             fence_after();
             const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                mma_f16(c.tmem + t.slot * kBufCols, desc_k_major(xs + 32 * i), desc_k_major(xs + kXBytes + 32 * i), id,
-                        !(fresh && i == 0));
+            for (int i = 0; i < 8; i++)
+                mma_f16(c.tmem + t.slot * kBufCols, desc_k_major(xs + (i >> 2) * (128 * 128) + 32 * (i & 3)),
+                        desc_k_major(xs + kXBytes + (i >> 2) * (rp * 128) + 32 * (i & 3)), id, !(fresh && i == 0));
             mma_commit(&c.empty[get.slot]);
             get.next(nslots);
             fresh = false;
