@@ -116,12 +116,13 @@ def lib():
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _bytes(t):
@@ -307,11 +308,13 @@ class DeviceAdapters:
         self.t_B = torch.tensor([b.data_ptr() for b in self.B], dtype=torch.int64, device=device)
         self.t_rank = torch.tensor(self.ranks, dtype=torch.int32, device=device)
         self.t_scale = torch.tensor(list(scales), dtype=torch.float32, device=device)
+        self._struct = exl3_adapters(self.t_A.data_ptr(), self.t_B.data_ptr(),
+                                     self.t_rank.data_ptr(), self.t_scale.data_ptr(), self.N,
+                                     self.max_rank, self.in_features, self.out_features)
+        self._ref = ctypes.byref(self._struct)     # built once: a decode call is short
 
     def struct(self) -> exl3_adapters:
-        return exl3_adapters(self.t_A.data_ptr(), self.t_B.data_ptr(), self.t_rank.data_ptr(),
-                             self.t_scale.data_ptr(), self.N, self.max_rank, self.in_features,
-                             self.out_features)
+        return self._struct
 
 
 # --------------------------------------------------------------------------- entry points
@@ -357,9 +360,9 @@ def exl3_moe_additive(x, ids, rw, experts: DeviceExperts, stages: DeviceStages, 
 
 
 def _shaped(what, t, shape, dtype=None):
-    if t is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous() or
-                          (dtype is not None and t.dtype != dtype)):
-        raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor"
+    if t is not None and (t.shape != shape or not t.is_contiguous() or
+                          (dtype is not None and t.dtype is not dtype)):
+        raise ValueError(f"{what} must be a contiguous {shape} tensor"
                          f"{'' if dtype is None else ' of ' + str(dtype)}")
 
 
@@ -415,8 +418,7 @@ def exl3_lora_forward(x, plan, adapters: DeviceAdapters, y, workspace, base=None
     _shaped("y", y, (M, adapters.out_features), dt)
     _shaped("base", base, (M, adapters.out_features), dt)
     _shaped("h", h, (M, adapters.h_cols), dt)
-    st = adapters.struct()
-    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, ctypes.byref(st), _ptr(plan), _ptr(base),
+    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, adapters._ref, _ptr(plan), _ptr(base),
                                 _ptr(y), _ptr(h), _ptr(workspace), _bytes(workspace),
                                 _stream(stream))
     return _check("exl3_lora_forward", rc, raise_on_error)
@@ -432,11 +434,9 @@ def exl3_lora_backward(dy, x, h, plan, adapters: DeviceAdapters, grads, workspac
     _shaped("dx_base", dx_base, (M, adapters.in_features), dt)
     if grads is not None and (grads.ranks != adapters.ranks or grads.dtype != dt):
         raise ValueError("grads must hold a tensor like A and one like B for every adapter")
-    st = adapters.struct()
-    gs = None if grads is None else grads.struct()
-    rc = _lib.exl3_lora_backward(_ptr(dy), _ptr(x), _ptr(h), _DTYPE[dt], M, ctypes.byref(st),
+    rc = _lib.exl3_lora_backward(_ptr(dy), _ptr(x), _ptr(h), _DTYPE[dt], M, adapters._ref,
                                  _ptr(plan), _ptr(dx_base), _ptr(dx),
-                                 None if gs is None else ctypes.byref(gs), _ptr(workspace),
+                                 None if grads is None else grads._ref, _ptr(workspace),
                                  _bytes(workspace), _stream(stream))
     return _check("exl3_lora_backward", rc, raise_on_error)
 

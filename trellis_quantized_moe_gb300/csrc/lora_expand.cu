@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         put.slot = done.slot = group;
         bool ok = true;
         int pending = 0, rank = 0, rp = 0;
-        size_t off[kN];
-        uint32_t in = 0;                           // bit i: row r0 + i kStep is in the tile
+        int row[kN], next_row[kN];                 // rows r0 + i kStep of this tile and the next; -1: none
+        const size_t pitch = (size_t)a.width * 2;
         const uint8_t *W = nullptr;
         auto finish = [&]() {                      // the oldest item in flight has landed
             fence_proxy();
@@ -182,37 +182,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             done.next2(g.nslots);
             pending--;
         };
-        int tile = -1;
+        // a tile's rows are looked up one tile ahead, its descriptor two
+        int tile = -1, known = (begin + group) / nb;           // known: the tile next_t describes
+        const int last_tile = (end - 1) / nb;
+        int4 next_t = tiles[min(known, last_tile)], next2_t = tiles[min(known + 1, last_tile)];
+        auto look_up = [&]() {
+#pragma unroll
+            for (int i = 0; i < kN; i++)
+                next_row[i] = a.base && r0 + i * kStep < next_t.z ? perm[next_t.y + r0 + i * kStep] : -1;
+        };
+        look_up();
         for (int s = begin + group; s < end; s += 2) {
             if (s / nb != tile) {
                 tile = s / nb;
-                const int4 t = tiles[tile];
-                rank = tile_rank(t);
-                rp = (rank + 15) / 16 * 16;
-                W = rank ? reinterpret_cast<const uint8_t *>(a.W[t.x]) + ((size_t)r0 * a.width + ch * 8) * 2 : nullptr;
-                in = 0;
-#pragma unroll
-                for (int i = 0; i < kN; i++) {
-                    const int r = r0 + i * kStep;
-                    off[i] = 0;
-                    if (a.base && r < t.z) {
-                        in |= 1u << i;
-                        off[i] = ((size_t)perm[t.y + r] * a.width + ch * 8) * 2;
-                    }
+                if (tile != known) {                           // nb = 1: a tile was the other group's
+                    next_t = next2_t;
+                    look_up();
+                    next2_t = tiles[min(tile + 1, last_tile)];
                 }
+                rank = tile_rank(next_t);
+                rp = (rank + 15) / 16 * 16;
+                W = rank ? reinterpret_cast<const uint8_t *>(a.W[next_t.x]) + r0 * pitch + ch * 16 : nullptr;
+#pragma unroll
+                for (int i = 0; i < kN; i++)
+                    row[i] = next_row[i];
+                next_t = next2_t;
+                look_up();
+                known = tile + 1;
+                next2_t = tiles[min(tile + 2, last_tile)];
             }
             if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
                 break;
             const size_t col = (size_t)(s - tile * nb) * (NW * 2);
             const uint32_t dst = smem_addr(ring + put.slot * g.slot_bytes), db = dst + r0 * g.pitch + ch * 16;
-            const uint8_t *base = static_cast<const uint8_t *>(a.base) + col;
+            const uint8_t *base = static_cast<const uint8_t *>(a.base) + col + ch * 16;
 #pragma unroll
             for (int i = 0; i < kN; i++)
-                if (in >> i & 1)
-                    cp_async16(db + i * kStep * g.pitch, base + off[i], true);
+                if (row[i] >= 0)
+                    cp_async16(db + i * kStep * g.pitch, base + row[i] * pitch, true);
             const uint32_t dw = dst + g.row_bytes + (ch >> 3) * (rp * 128);
             const uint8_t *w = W + col;
-            for (int j = r0; j < rp; j += kStep, w += (size_t)kStep * a.width * 2)
+            for (int j = r0; j < rp; j += kStep, w += kStep * pitch)
                 cp_async16(dw + swz(j, ch & 7), j < rank ? w : W, j < rank);
             cp_async_commit();
             put.next2(g.nslots);

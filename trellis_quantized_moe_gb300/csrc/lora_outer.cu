@@ -179,9 +179,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                 row[i] = r < rows && xin ? perm[slot0 + r] : -1;
             }
         };
+        int e_known = -1;
         auto enter = [&](int k) {
-            slot0 = offs[it.e];
-            rows = offs[it.e + 1] - slot0;
+            if (it.e != e_known) {
+                e_known = it.e;
+                slot0 = offs[it.e];
+                rows = offs[it.e + 1] - slot0;
+            }
             x = static_cast<const uint8_t *>(a.p[it.p].x) + (size_t)it.n * (2 * kOuterN) + ch * 16;
             xin = it.n * kOuterN + ch * 8 < a.p[it.p].width;
             h = static_cast<const uint8_t *>(a.p[it.p].h);

@@ -30,6 +30,7 @@ EXL3_DEV int scan_exclusive(int v, int *sums, int *total)
         sums[warp] = x;
     __syncthreads();
     int before = 0, all = 0;
+#pragma unroll 8
     for (int w = 0; w < kWarps; w++) {
         before += w < warp ? sums[w] : 0;
         all += sums[w];
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_plan(LoraPlanArgs a)
     // group g = tid: its size; the warps' counts become offsets inside it
     int rows = 0;
     if (tid < N)
+#pragma unroll 8
         for (int w = 0; w < kWarps; w++) {
             const int c = hist[w * G + tid];
             hist[w * G + tid] = rows;

@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         const int group = warp >> 2, gt = tid & 127, ch = gt & 15, r0 = gt >> 4;
         const int lag = loader_lag(nslots);
         const size_t wstep = (size_t)a.width * 16;             // 8 rows of W
-        size_t off[16];
-        uint32_t in = 0;                           // bit i: row r0 + 8 i is in the tile
+        int row[16], next_row[16];                 // rows r0 + 8 i of this tile and the next; -1: none
         const uint8_t *w = nullptr;
+        const size_t pitch = (size_t)a.width * 2;
         int rank = 0, rp = 16, pending = 0;
         Ring put, done;
         put.slot = done.slot = group;
@@ -129,31 +129,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             pending--;
         };
         int tile = (begin + group) / ks, k = (begin + group) % ks;
+        // A tile's rows are looked up one tile ahead, its descriptor two: a
+        // look-up in the open drains the ring for two memory latencies.
+        const int last_tile = (end - 1) / ks;
+        int4 next_t = tiles[min(tile, last_tile)], next2_t = tiles[min(tile + 1, last_tile)];
+        auto look_up = [&]() {
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                next_row[i] = r0 + 8 * i < next_t.z ? perm[next_t.y + r0 + 8 * i] : -1;
+        };
+        look_up();
         bool fresh = true, ok = true;
         for (int s = begin + group; s < end; s += 2) {
             if (fresh) {
-                const int4 t = tiles[tile];
-                rank = tile_rank(t.x);
+                rank = tile_rank(next_t.x);
                 rp = max(16, (rank + 15) / 16 * 16);
-                w = reinterpret_cast<const uint8_t *>(a.W[t.x]) + (size_t)r0 * a.width * 2 + ch * 16;
-                in = 0;
+                w = reinterpret_cast<const uint8_t *>(a.W[next_t.x]) + (size_t)r0 * pitch + ch * 16;
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int r = r0 + 8 * i;
-                    in |= (uint32_t)(r < t.z) << i;
-                    off[i] = r < t.z ? ((size_t)perm[t.y + r] * a.width + ch * 8) * 2 : 0;
-                }
+                for (int i = 0; i < 16; i++)
+                    row[i] = next_row[i];
+                next_t = next2_t;
+                look_up();
+                next2_t = tiles[min(tile + 2, last_tile)];
                 fresh = false;
             }
             if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
-            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 256;
+            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 256 + ch * 16;
             // 64-wide block ch / 8, row r0 + 8 i, chunk ch % 8
             const uint32_t dx = dst + (ch >> 3) * (128 * 128) + swz(r0, ch & 7);
 #pragma unroll
             for (int i = 0; i < 16; i++)
-                cp_async16(dx + i * 1024, x + off[i], in >> i & 1);
+                cp_async16(dx + i * 1024, row[i] < 0 ? x : x + row[i] * pitch, row[i] >= 0);
             const uint8_t *wk = w + (size_t)k * 256;
             const uint32_t dw = dst + kXBytes + (ch >> 3) * (rp * 128) + swz(r0, ch & 7);
             for (int i = 0; i < rp / 8; i++, wk += wstep) {
@@ -167,10 +175,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 finish();
             }
             k += 2;
-            while (k >= ks) {                      // ks may be 1
-                k -= ks;
-                tile++;
+            if (k >= ks) {
                 fresh = true;
+                tile++;
+                k -= ks;
+                if (k >= ks) {                     // ks = 1: this group skips a tile
+                    tile++;
+                    k -= ks;
+                    next_t = next2_t;
+                    look_up();
+                    next2_t = tiles[min(tile + 1, last_tile)];
+                }
             }
         }
         cp_async_wait<0>();
