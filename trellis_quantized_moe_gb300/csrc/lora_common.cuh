@@ -29,9 +29,14 @@ EXL3_DEV void cp_async16(uint32_t dst, const void *src, bool valid)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
                  : "memory");
 }
-EXL3_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-EXL3_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+EXL3_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrives on `bar` when the thread's copies so far have landed.  The reader
+// then runs the proxy fence: one in the copying threads waits for every copy
+// they have in flight (16384-row shrink: 40 us with it there, whatever the ring).
+EXL3_DEV void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 EXL3_DEV void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 EXL3_DEV uint32_t swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
@@ -53,6 +58,25 @@ EXL3_DEV uint32_t idesc(int n, int act_dtype, int ta, int tb)
     const uint32_t f = act_dtype == EXL3_BF16 ? 1u : 0u;
     return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) |
            ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+// 32 accumulator columns of the warp's lane quarter.
+EXL3_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
 EXL3_DEV void tmem_alloc(uint32_t *dst, uint32_t cols)
@@ -87,19 +111,6 @@ EXL3_DEV float2 unpack2(uint32_t u, int dtype)
 EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
 {
     return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;
-}
-
-// cp.async.wait_group for a count known at run time (1..4).
-EXL3_DEV void cp_async_wait_n(int n)
-{
-    if (n >= 4)
-        cp_async_wait<4>();
-    else if (n == 3)
-        cp_async_wait<3>();
-    else if (n == 2)
-        cp_async_wait<2>();
-    else
-        cp_async_wait<1>();
 }
 
 // Launch that may start while the kernel before it in the stream still runs;
@@ -140,11 +151,6 @@ struct Ring {
         }
     }
 };
-
-// Stages a loader group keeps in flight beyond the one it issues, two groups
-// taking turns on a ring of n slots: n > 2 * lag, so that a group never waits
-// for a slot whose stage only a later step of its own would hand over.
-EXL3_HD inline int loader_lag(int n) { return n >= 10 ? 4 : n >= 8 ? 3 : n >= 6 ? 2 : 1; }
 
 }  // namespace lora
 }  // namespace exl3

@@ -20,7 +20,9 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 544;       // 8 loader, 4 epilogue warps, MMA warp, 4 join warps
+constexpr int kThreads = 640;       // 8 loader, 8 epilogue warps, MMA warp, 3 join warps
+constexpr int kMmaWarp = 16, kJoinWarp = 17;
+constexpr int kFirstJoin = 352;     // threads that join a CTA's first tile: epilogue and join warps
 constexpr int kTBufs = 4;           // TMEM accumulators
 constexpr int kMaxRing = 4;
 
@@ -45,23 +47,23 @@ EXL3_HD inline Geom geom(int h_cols)
 EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
 
 struct Ctl {
-    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
+    uint64_t hfirst, hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
     uint32_t tmem;
     int abort;
 };
 
-// Joins h of one tile, thread jt of 128: the partials of CTAs c0..c1 in that
-// order, scaled, zero from the rank on, rounded; into shared memory (hs) and,
-// with keep, into a.h.  A thread has four columns of up to eight rows in
-// flight: the partials lie in L2, and one load at a time took longer (r = 128:
-// 40 us a tile) than everything else in the kernel.
+// Joins h of one tile, thread jt of n (a multiple of 32): the partials of CTAs
+// c0..c1 in that order, scaled, zero from the rank on, rounded; into shared
+// memory (hs) and, with keep, into a.h.  A thread has four columns of up to
+// eight rows of two partials in flight: they lie in L2, and one load at a time
+// took longer (r = 128: 40 us a tile) than everything else in the kernel.
 EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, int c1, float alpha, uint8_t *hs,
-                     bool keep, int jt)
+                     bool keep, int jt, int n)
 {
     constexpr int kU = 8;
     const int rp = (rank + 15) / 16 * 16;
     const int lq = rp <= 16 ? 2 : rp <= 32 ? 3 : rp <= 64 ? 4 : 5;   // lanes per row: 2^lq
-    const int j = (jt & ((1 << lq) - 1)) * 4, step = 128 >> lq;
+    const int j = (jt & ((1 << lq) - 1)) * 4, step = n >> lq;
     if (j >= rp)
         return;
     const size_t cta = 128 * (size_t)a.h_cols;
@@ -72,12 +74,14 @@ EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, i
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float *p = a.part + (size_t)(t.y + r0) * a.h_cols + j + c0 * cta;
         for (int c = c0; c <= c1; c++, p += cta) {
+            float4 f[kU];
 #pragma unroll
             for (int u = 0; u < kU; u++)
-                if (r0 + u * step < t.z) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p + (size_t)u * step * a.h_cols);
-                    v[u].x += f.x; v[u].y += f.y; v[u].z += f.z; v[u].w += f.w;
-                }
+                f[u] = *reinterpret_cast<const float4 *>(p + (size_t)min(u * step, t.z - 1 - r0) * a.h_cols);
+#pragma unroll
+            for (int u = 0; u < kU; u++) {
+                v[u].x += f[u].x; v[u].y += f[u].y; v[u].z += f[u].z; v[u].w += f[u].w;
+            }
         }
 #pragma unroll
         for (int u = 0; u < kU; u++) {
@@ -134,22 +138,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     uint8_t *hbuf = smem, *ring = smem + 2 * g.h_bytes;
     volatile int *abort = &c.abort;
     if (tid == 0) {
+        mbar_init(&c.hfirst, kFirstJoin);
         for (int i = 0; i < 2; i++) {
-            mbar_init(&c.hfull[i], 128);
+            mbar_init(&c.hfull[i], 96);
             mbar_init(&c.hempty[i], 1);
         }
         for (int i = 0; i < kMaxRing; i++) {
             mbar_init(&c.full[i], 128);
-            mbar_init(&c.empty[i], 128);
+            mbar_init(&c.empty[i], 256);
         }
         for (int i = 0; i < kTBufs; i++) {
             mbar_init(&c.tfull[i], 1);
-            mbar_init(&c.tempty[i], 128);
+            mbar_init(&c.tempty[i], 256);
         }
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 12)
+    if (warp == kMmaWarp)
         tmem_alloc(&c.tmem, NW * kTBufs);
     fence_before();
     __syncthreads();
@@ -169,19 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         // group 0 takes the even items of the share, group 1 the odd ones
         constexpr int kLanes = NW / 8, kStep = 128 / kLanes, kN = 128 / kStep;   // lanes per row, rows a pass
         const int group = warp >> 2, gt = tid & 127, ch = gt % kLanes, r0 = gt / kLanes;
-        Ring put, done;
-        put.slot = done.slot = group;
-        bool ok = true;
-        int pending = 0, rank = 0, rp = 0;
+        Ring put;
+        put.slot = group;
+        int rank = 0, rp = 0;
         int row[kN], next_row[kN];                 // rows r0 + i kStep of this tile and the next; -1: none
         const size_t pitch = (size_t)a.width * 2;
         const uint8_t *W = nullptr;
-        auto finish = [&]() {                      // the oldest item in flight has landed
-            fence_proxy();
-            mbar_arrive(&c.full[done.slot]);
-            done.next2(g.nslots);
-            pending--;
-        };
         // a tile's rows are looked up one tile ahead, its descriptor two
         int tile = -1, known = (begin + group) / nb;           // known: the tile next_t describes
         const int last_tile = (end - 1) / nb;
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 known = tile + 1;
                 next2_t = tiles[min(tile + 2, last_tile)];
             }
-            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+            if (!wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr))
                 break;
             const size_t col = (size_t)(s - tile * nb) * (NW * 2);
             const uint32_t dst = smem_addr(ring + put.slot * g.slot_bytes), db = dst + r0 * g.pitch + ch * 16;
@@ -224,17 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             const uint8_t *w = W + col;
             for (int j = r0; j < rp; j += kStep, w += kStep * pitch)
                 cp_async16(dw + swz(j, ch & 7), j < rank ? w : W, j < rank);
-            cp_async_commit();
+            cp_async_arrive(&c.full[put.slot]);
             put.next2(g.nslots);
-            if (++pending > 1) {                   // two groups, four slots: one more in flight each
-                cp_async_wait<1>();
-                finish();
-            }
         }
-        cp_async_wait<0>();
-        while (ok && pending)
-            finish();
-    } else if (warp >= 13) {
+        cp_async_wait_all();
+    } else if (warp >= kJoinWarp) {
         grid_dep_wait();                           // the partials and the error word
         const bool bad = a.hdr[kHdrError] != 0;
         Ring hb;
@@ -245,29 +237,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             if (rank > 0) {
                 const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
                 const int c0 = tile * sks / sper, c1 = ((tile + 1) * sks - 1) / sper;
+                const bool first = a.y && s == begin;
                 if (a.y && !wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
                     break;
                 if (!bad)
                     join_h(a, t, rank, c0, c1, alpha, a.y ? hbuf + hb.slot * g.h_bytes : nullptr,
-                           a.h != nullptr && s % nb == 0, tid - 416);
+                           a.h != nullptr && s % nb == 0, tid - kJoinWarp * 32, first ? kFirstJoin : 96);
                 if (a.y) {
                     fence_proxy();
-                    mbar_arrive(&c.hfull[hb.slot]);
+                    mbar_arrive(first ? &c.hfirst : &c.hfull[hb.slot]);
                     hb.next(2);
                 }
             }
             s = last;
         }
-    } else if (warp >= 8 && warp < 12 && a.y) {
-        constexpr int kLanes = NW / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
-        const int q = warp & 3, row = 32 * q + lane;
-        grid_dep_wait();                           // the error word
+    } else if (warp >= 8 && warp < kMmaWarp && a.y) {
+        // warps 8 + q and 12 + q: rows 32 q .. 32 q + 31, half the columns each
+        constexpr int kCols = NW / 2, kLanes = kCols / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
+        const int q = warp & 3, c0 = (warp - 8) / 4 * kCols, row = 32 * q + lane;
+        grid_dep_wait();                           // the error word and the partials
         const bool bad = a.hdr[kHdrError] != 0;
         Ring t4, in;
         for (int s = begin; s < end;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
             const int4 t = tiles[tile];
-            const bool mma = tile_rank(t) > 0;
+            const int rank = tile_rank(t);
+            const bool mma = rank > 0;
+            if (mma && s == begin) {
+                // nothing to do before the first tile's h is there: help joining it
+                if (!bad)
+                    join_h(a, t, rank, tile * sks / sper, ((tile + 1) * sks - 1) / sper,
+                           a.scale_h ? a.scale[t.x] : 1.0f, hbuf, a.h != nullptr && s % nb == 0, tid - 160, kFirstJoin);
+                fence_proxy();
+                mbar_arrive(&c.hfirst);
+            }
             const float alpha = mma && !a.scale_h ? a.scale[t.x] : 1.0f;
             const size_t off = row < t.z ? (size_t)perm[t.y + row] * a.width * 2 : 0;
             const int rows = bad ? 0 : min(32, t.z - 32 * q);      // of this warp, to be written
@@ -278,19 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 if (!(ok = __all_sync(0xffffffffu, ok)))
                     break;
                 fence_after();
-                uint8_t *warp_rows = ring + in.slot * g.slot_bytes + 32 * q * g.pitch;
+                uint8_t *warp_rows = ring + in.slot * g.slot_bytes + 32 * q * g.pitch + c0 * 2;
                 uint8_t *mine = warp_rows + lane * g.pitch;
-                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * NW;
+                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * NW + c0;
                 if (mma || !a.base) {
 #pragma unroll
-                    for (int n = 0; n < NW; n += 16) {
-                        uint32_t v[16] = {};
-                        if (mma) {
-                            tmem_ld16_issue(acc + n, v);
-                            tmem_ld16_wait(v);
-                        }
+                    for (int n = 0; n < kCols; n += 32) {
+                        uint32_t v[32] = {};
+                        if (mma)
+                            tmem_ld32(acc + n, v);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 8) {
+                        for (int i = 0; i < 32; i += 8) {
                             uint4 u = make_uint4(0, 0, 0, 0);
                             if (a.base)
                                 u = *reinterpret_cast<const uint4 *>(mine + (n + i) * 2);
@@ -311,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     t4.next(kTBufs);
                 }
                 __syncwarp();
-                uint8_t *out = static_cast<uint8_t *>(a.y) + (size_t)(s - tile * nb) * (NW * 2) + lane % kLanes * 16;
-#pragma unroll 8
+                uint8_t *out = static_cast<uint8_t *>(a.y) + (size_t)(s - tile * nb) * (NW * 2) + c0 * 2 +
+                               lane % kLanes * 16;
+#pragma unroll
                 for (int r0 = 0; r0 < 32; r0 += kRows) {
                     const int r = r0 + lane / kLanes;
                     const size_t o = __shfl_sync(0xffffffffu, off, r);
@@ -328,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         }
         if (bad)
             zero_fill(tid - 256);
-    } else if (warp == 12 && lane == 0 && a.y) {
+    } else if (warp == kMmaWarp && lane == 0 && a.y) {
         Ring hb, in, t4;
+        uint32_t hphase[2] = {0, 0};               // the first tile takes a slot without its hfull
         bool ok = true;
         for (int s = begin; s < end && ok;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
@@ -340,13 +343,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 continue;
             }
             const uint32_t id = idesc(NW, a.act_dtype, 0, 1);
-            if (!(ok = wait_bar(&c.hfull[hb.slot], hb.phase, abort, a.hdr)))
+            const bool first = s == begin;
+            if (!(ok = wait_bar(first ? &c.hfirst : &c.hfull[hb.slot], first ? 0 : hphase[hb.slot], abort, a.hdr)))
                 break;
+            if (!first)
+                hphase[hb.slot] ^= 1;
             const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
             for (; s < last; s++) {
                 if (!(ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr) &&
                            wait_bar(&c.tempty[t4.slot], t4.phase ^ 1, abort, a.hdr)))
                     break;
+                fence_proxy();
                 fence_after();
                 const uint32_t ws = smem_addr(ring + in.slot * g.slot_bytes + g.row_bytes);
                 for (int k = 0; k < rp / 16; k++)
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     __syncthreads();
     fence_after();
     __syncwarp();
-    if (warp == 12)
+    if (warp == kMmaWarp)
         tmem_free(c.tmem, NW * kTBufs);
 }
 

@@ -156,17 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         // group 0 takes the even stages of the share, group 1 the odd ones
         const int group = warp >> 2, gt = tid & 127;
         const int ch = gt & 31, r0 = gt >> 5;       // a warp per 512-byte row of x
-        const int lag = loader_lag(nslots);
-        Ring put, done;
-        put.slot = done.slot = group;
-        int pending = 0;
-        auto finish = [&]() {
-            fence_proxy();
-            mbar_arrive(&c.full[done.slot]);
-            done.next2(nslots);
-            pending--;
-        };
-        bool ok = true;
+        Ring put;
+        put.slot = group;
         int row[16], slot0 = 0, rows = 0;            // rows of the current stage (-1: past the end)
         int hq = 0, hr = 0, hrows = 64, hn = 1;     // h: this thread's chunk, row, row step, passes
         bool hin = true, xin = true;                 // xin: this thread's chunk is in the item
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             enter(k);
         }
         for (int s = begin + group; s < end; s += 2) {
-            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+            if (!wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr))
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
 #pragma unroll
@@ -230,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                     cp_async16(dst + kXBytes + (hq >> 3) * kBlock + swz(r, hq & 7),
                                v ? hk + (size_t)i * hrows * a.h_cols * 2 : static_cast<const uint8_t *>(a.p[0].x), v);
                 }
-            cp_async_commit();
+            cp_async_arrive(&c.full[put.slot]);
             put.next2(nslots);
             if (s + 2 < end) {
                 k += 2;
@@ -239,14 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                 else
                     load_rows(k);
             }
-            if (++pending > lag) {
-                cp_async_wait_n(lag);
-                finish();
-            }
         }
-        cp_async_wait<0>();
-        while (ok && pending)
-            finish();
+        cp_async_wait_all();
     } else if (warp < 12) {
         const int q = warp & 3, col = 32 * q + lane;
         Ring t;
@@ -301,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             for (; s < stop; s++) {
                 if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
                     break;
+                fence_proxy();
                 fence_after();
                 const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
                 for (int half = 0; half < halves; half++)

@@ -9,9 +9,7 @@
 // one fp32 partial per CTA, which the expand kernel adds in CTA order.  A stage
 // is 128 rows x 256 bytes of x and the adapter's rank x 256 bytes of W, copied
 // by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring by two
-// groups of loader warps that take turns, since a stage's copies, wait, proxy
-// fence and arrival in one group take longer than its share of HBM time; one
-// thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
+// groups of loader warps that take turns; one thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
 // warps drain the accumulator, double-buffered in TMEM.
 #include "lora_common.cuh"
 
@@ -20,7 +18,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
+constexpr int kThreads = 448;       // 8 loader warps in two groups, 4 epilogue warps, MMA, check warp
 constexpr int kXBytes = 2 * 128 * 128;   // two 64-wide blocks
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 6;
@@ -39,7 +37,8 @@ struct Ctl {
     int abort;
 };
 
-// CTA 0: the tables of every adapter in use
+// The tables of every adapter in use, by one warp of CTA 0 (the others start
+// on their rows meanwhile).
 __device__ void check_tables(const LoraShrinkArgs &a)
 {
     int err;
@@ -48,7 +47,8 @@ __device__ void check_tables(const LoraShrinkArgs &a)
     } else {
         err = a.plan[kLpError];
         const int32_t *off = a.plan + lora_plan_layout(a.M, a.N).offsets / 4;
-        for (int i = threadIdx.x; i < a.N; i += kThreads) {
+#pragma unroll 4
+        for (int i = threadIdx.x & 31; i < a.N; i += 32) {
             if (off[i] == off[i + 1] && !a.GA)
                 continue;
             const int r = a.rank[i];
@@ -61,8 +61,8 @@ __device__ void check_tables(const LoraShrinkArgs &a)
             err |= bad ? EXL3_DERR_TABLE : 0;
         }
     }
-    const int table = __syncthreads_or(err & EXL3_DERR_TABLE);
-    if (threadIdx.x == 0)
+    const bool table = __any_sync(0xffffffffu, err & EXL3_DERR_TABLE);
+    if ((threadIdx.x & 31) == 0)
         a.hdr[kHdrError] = err | (table ? EXL3_DERR_TABLE : 0);
 }
 
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     __shared__ Ctl c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_launch();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && warp == 13)
         check_tables(a);
     if (!plan_ok(a.plan, a.M, a.N))
         return;
@@ -114,20 +114,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     if (warp < 8) {
         // group 0 takes the even stages of the share, group 1 the odd ones
         const int group = warp >> 2, gt = tid & 127, ch = gt & 15, r0 = gt >> 4;
-        const int lag = loader_lag(nslots);
         const size_t wstep = (size_t)a.width * 16;             // 8 rows of W
         int row[16], next_row[16];                 // rows r0 + 8 i of this tile and the next; -1: none
         const uint8_t *w = nullptr;
         const size_t pitch = (size_t)a.width * 2;
-        int rank = 0, rp = 16, pending = 0;
-        Ring put, done;
-        put.slot = done.slot = group;
-        auto finish = [&]() {                      // the oldest stage in flight has landed
-            fence_proxy();
-            mbar_arrive(&c.full[done.slot]);
-            done.next2(nslots);
-            pending--;
-        };
+        int rank = 0, rp = 16;
+        Ring put;
+        put.slot = group;
         int tile = (begin + group) / ks, k = (begin + group) % ks;
         // A tile's rows are looked up one tile ahead, its descriptor two: a
         // look-up in the open drains the ring for two memory latencies.
@@ -139,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 next_row[i] = r0 + 8 * i < next_t.z ? perm[next_t.y + r0 + 8 * i] : -1;
         };
         look_up();
-        bool fresh = true, ok = true;
+        bool fresh = true;
         for (int s = begin + group; s < end; s += 2) {
             if (fresh) {
                 rank = tile_rank(next_t.x);
@@ -153,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 next2_t = tiles[min(tile + 2, last_tile)];
                 fresh = false;
             }
-            if (!(ok = wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr)))
+            if (!wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr))
                 break;
             const uint32_t dst = smem_addr(smem + (size_t)put.slot * sbytes);
             const uint8_t *x = static_cast<const uint8_t *>(a.x) + (size_t)k * 256 + ch * 16;
@@ -168,12 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 const bool v = r0 + 8 * i < rank;
                 cp_async16(dw + i * 1024, v ? wk : static_cast<const uint8_t *>(a.x), v);
             }
-            cp_async_commit();
+            cp_async_arrive(&c.full[put.slot]);
             put.next2(nslots);
-            if (++pending > lag) {
-                cp_async_wait_n(lag);
-                finish();
-            }
             k += 2;
             if (k >= ks) {
                 fresh = true;
@@ -188,9 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 }
             }
         }
-        cp_async_wait<0>();
-        while (ok && pending)
-            finish();
+        cp_async_wait_all();
     } else if (warp < 12) {
         const int q = warp & 3, row = 32 * q + lane;
         int tile = begin / ks;
@@ -217,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             t.next(2);
             s = (tile + 1) * ks;
         }
-    } else if (lane == 0) {
+    } else if (warp == 12 && lane == 0) {
         int tile = begin / ks, k = begin % ks;
         Ring get, t;
         uint32_t id = 0;
@@ -233,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             }
             if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
                 break;
+            fence_proxy();
             fence_after();
             const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
 #pragma unroll
