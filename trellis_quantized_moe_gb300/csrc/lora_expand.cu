@@ -68,19 +68,31 @@ EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, i
         return;
     const size_t cta = 128 * (size_t)a.h_cols;
     for (int r0 = jt >> lq; r0 < t.z; r0 += kU * step) {
-        float4 v[kU];
+        float4 v[kU], f[kU];
 #pragma unroll
         for (int u = 0; u < kU; u++)
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float *p = a.part + (size_t)(t.y + r0) * a.h_cols + j + c0 * cta;
-        for (int c = c0; c <= c1; c++, p += cta) {
-            float4 f[kU];
+        if (t.z <= step) {                         // one row a thread: eight partials in flight
+            for (int c = c0; c <= c1; c += kU, p += kU * cta) {
 #pragma unroll
-            for (int u = 0; u < kU; u++)
-                f[u] = *reinterpret_cast<const float4 *>(p + (size_t)min(u * step, t.z - 1 - r0) * a.h_cols);
+                for (int u = 0; u < kU; u++)
+                    f[u] = *reinterpret_cast<const float4 *>(p + min(u, c1 - c) * cta);
 #pragma unroll
-            for (int u = 0; u < kU; u++) {
-                v[u].x += f[u].x; v[u].y += f[u].y; v[u].z += f[u].z; v[u].w += f[u].w;
+                for (int u = 0; u < kU; u++)
+                    if (c + u <= c1) {
+                        v[0].x += f[u].x; v[0].y += f[u].y; v[0].z += f[u].z; v[0].w += f[u].w;
+                    }
+            }
+        } else {
+            for (int c = c0; c <= c1; c++, p += cta) {
+#pragma unroll
+                for (int u = 0; u < kU; u++)
+                    f[u] = *reinterpret_cast<const float4 *>(p + (size_t)min(u * step, t.z - 1 - r0) * a.h_cols);
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
+                    v[u].x += f[u].x; v[u].y += f[u].y; v[u].z += f[u].z; v[u].w += f[u].w;
+                }
             }
         }
 #pragma unroll
@@ -88,10 +100,10 @@ EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, i
             const int r = r0 + u * step;
             if (r >= t.z)
                 break;
-            const float4 f = v[u];
+            const float4 w = v[u];
             const uint2 o = make_uint2(
-                pack2(j < rank ? f.x * alpha : 0.f, j + 1 < rank ? f.y * alpha : 0.f, a.act_dtype),
-                pack2(j + 2 < rank ? f.z * alpha : 0.f, j + 3 < rank ? f.w * alpha : 0.f, a.act_dtype));
+                pack2(j < rank ? w.x * alpha : 0.f, j + 1 < rank ? w.y * alpha : 0.f, a.act_dtype),
+                pack2(j + 2 < rank ? w.z * alpha : 0.f, j + 3 < rank ? w.w * alpha : 0.f, a.act_dtype));
             if (hs)
                 *reinterpret_cast<uint2 *>(hs + (j >> 6) * (128 * 128) + swz(r, (j & 63) >> 3) + (j & 4) * 2) = o;
             if (keep)
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 uint8_t *warp_rows = ring + in.slot * g.slot_bytes + 32 * q * g.pitch + c0 * 2;
                 uint8_t *mine = warp_rows + lane * g.pitch;
                 const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * NW + c0;
-                if (mma || !a.base) {
+                if ((mma || !a.base) && rows > 0) {            // warps past the tile's rows only keep step
 #pragma unroll
                     for (int n = 0; n < kCols; n += 32) {
                         uint32_t v[32] = {};
@@ -316,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                                lane % kLanes * 16;
 #pragma unroll
                 for (int r0 = 0; r0 < 32; r0 += kRows) {
+                    if (r0 >= rows)
+                        break;
                     const int r = r0 + lane / kLanes;
                     const size_t o = __shfl_sync(0xffffffffu, off, r);
                     const uint4 u = *reinterpret_cast<const uint4 *>(warp_rows + r * g.pitch + lane % kLanes * 16);

@@ -19,7 +19,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 416;       // 8 loader warps in two groups, 4 epilogue warps, MMA warp
+constexpr int kThreads = 448;       // 8 loader warps in two groups, 4 epilogue, MMA, fence warp
 constexpr int kBlock = 64 * 128;                 // 64 rows of 64 columns
 constexpr int kXBytes = kOuterN / 64 * kBlock;
 constexpr int kHalfCols = 128;                   // TMEM columns of one 128-column half
@@ -37,7 +37,7 @@ EXL3_HD inline int ring_slots(int h_cols)
 }
 
 struct Ctl {
-    uint64_t full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
+    uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
     uint32_t tmem;
     int abort;
 };
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     if (tid == 32) {
         for (int i = 0; i < nslots; i++) {
             mbar_init(&c.full[i], 128);
+            mbar_init(&c.ready[i], 1);
             mbar_init(&c.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -147,12 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     __syncthreads();
     fence_after();
 
-    grid_dep_wait();                // dh and the error word come from the kernels before
-    const bool bad = a.hdr[kHdrError] != 0;
     Item it = start;
-    auto padded_rank = [&](int e) { return max(16, (a.rank[e] + 15) / 16 * 16); };
-    if (bad) {
-    } else if (warp < 8) {
+    // (a bad table entry is in the error word, which only the epilogue reads)
+    auto padded_rank = [&](int e) { return min(a.h_cols, max(16, (a.rank[e] + 15) / 16 * 16)); };
+    if (warp < 8) {
         // group 0 takes the even stages of the share, group 1 the odd ones
         const int group = warp >> 2, gt = tid & 127;
         const int ch = gt & 31, r0 = gt >> 5;       // a warp per 512-byte row of x
@@ -205,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             settle();
             enter(k);
         }
+        grid_dep_wait();            // h (dh) comes from the kernels before
         for (int s = begin + group; s < end; s += 2) {
             if (!wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr))
                 break;
@@ -235,10 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     } else if (warp < 12) {
         const int q = warp & 3, col = 32 * q + lane;
         Ring t;
+        grid_dep_wait();            // and so does the error word
+        const bool bad = a.hdr[kHdrError] != 0;
         for (int s = begin; s < end;) {
             const int stop = min(end, it.first + it.len);
             const bool whole = it.first >= begin && it.first + it.len <= end;
-            const int rank = a.rank[it.e], width = a.p[it.p].width;
+            const int rank = bad ? 0 : a.rank[it.e], width = a.p[it.p].width;
             const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
             void *out = rank > 0 ? reinterpret_cast<void *>(a.p[it.p].G[it.e]) : nullptr;
             float *part = a.part + (2 * (size_t)blockIdx.x + (s > begin)) * kOuterN * a.h_cols + col;
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             if (s < end)
                 next_item(a, steps, it);
         }
-    } else if (lane == 0) {
+    } else if (warp == 12 && lane == 0) {
         Ring get, t;
         bool ok = true;
         for (int s = begin; s < end && ok;) {
@@ -284,9 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             const int halves = min(2, (a.p[it.p].width - it.n * kOuterN) / 128);
             bool first = true;
             for (; s < stop; s++) {
-                if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
+                if (!(ok = wait_bar(&c.ready[get.slot], get.phase, abort, a.hdr)))
                     break;
-                fence_proxy();
                 fence_after();
                 const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
                 for (int half = 0; half < halves; half++)
@@ -303,6 +304,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             t.next(2);
             if (s < end)
                 next_item(a, steps, it);
+        }
+    } else if (warp == 13 && lane == 0) {
+        // the proxy fence between the copies and the MMAs, off the MMA
+        // thread's path (one thread, every stage in order: a thread that left
+        // stages out could meet a barrier a whole phase early)
+        Ring get;
+        for (int s = begin; s < end; s++) {
+            if (!wait_bar(&c.full[get.slot], get.phase, abort, a.hdr))
+                break;
+            fence_proxy();
+            mbar_arrive(&c.ready[get.slot]);
+            get.next(nslots);
         }
     }
     fence_before();

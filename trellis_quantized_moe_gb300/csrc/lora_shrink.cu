@@ -18,7 +18,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 448;       // 8 loader warps in two groups, 4 epilogue warps, MMA, check warp
+constexpr int kThreads = 480;       // 8 loader warps in two groups, 4 epilogue, MMA, fence, check warp
 constexpr int kXBytes = 2 * 128 * 128;   // two 64-wide blocks
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 6;
@@ -32,7 +32,7 @@ EXL3_HD inline int ring_slots(int h_cols)
 }
 
 struct Ctl {
-    uint64_t full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
+    uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
     uint32_t tmem;
     int abort;
 };
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     __shared__ Ctl c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_launch();
-    if (blockIdx.x == 0 && warp == 13)
+    if (blockIdx.x == 0 && warp == 14)
         check_tables(a);
     if (!plan_ok(a.plan, a.M, a.N))
         return;
@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     if (tid == 0) {
         for (int i = 0; i < nslots; i++) {
             mbar_init(&c.full[i], 128);
+            mbar_init(&c.ready[i], 1);
             mbar_init(&c.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -218,9 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                     break;
                 fence_after();
             }
-            if (!(ok = wait_bar(&c.full[get.slot], get.phase, abort, a.hdr)))
+            if (!(ok = wait_bar(&c.ready[get.slot], get.phase, abort, a.hdr)))
                 break;
-            fence_proxy();
             fence_after();
             const uint32_t xs = smem_addr(smem + (size_t)get.slot * sbytes);
 #pragma unroll
@@ -237,6 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 tile++;
                 fresh = true;
             }
+        }
+    } else if (warp == 13 && lane == 0) {
+        // the proxy fence between the copies and the MMAs, off the MMA
+        // thread's path (one thread, every stage in order: a thread that left
+        // stages out could meet a barrier a whole phase early)
+        Ring get;
+        for (int s = begin; s < end; s++) {
+            if (!wait_bar(&c.full[get.slot], get.phase, abort, a.hdr))
+                break;
+            fence_proxy();
+            mbar_arrive(&c.ready[get.slot]);
+            get.next(nslots);
         }
     }
     fence_before();
