@@ -9,6 +9,7 @@
 #include "host.h"
 #include "kernels.h"
 #include "lora.h"
+#include "router.h"
 
 using namespace exl3;
 
@@ -73,7 +74,8 @@ int setup_device(cudaStream_t s, int *dev_out, int *sms_out)
             return EXL3_E_CUDA;
         if (route_pack_set_attributes() != cudaSuccess || gemm_gateup_set_attributes() != cudaSuccess ||
             gemm_down_set_attributes() != cudaSuccess || gemm_linear_set_attributes() != cudaSuccess ||
-            tc_set_attributes() != cudaSuccess || lora_set_attributes() != cudaSuccess)
+            tc_set_attributes() != cudaSuccess || lora_set_attributes() != cudaSuccess ||
+            router_set_attributes() != cudaSuccess)
             return EXL3_E_CUDA;
         d.ready = true;
     }

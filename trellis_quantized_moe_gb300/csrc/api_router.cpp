@@ -68,9 +68,8 @@ int exl3_router_forward(const void *logits, int logits_dtype, int M, int E, int 
     a.counts = counts;
     a.loss = loss;
     if (counts) {
-        a.mean = static_cast<float *>(ws);
-        if (!a.stats)
-            a.stats = a.mean + (E + 1) / 2 * 2;
+        a.psum = static_cast<float *>(ws);
+        a.pcount = reinterpret_cast<int32_t *>(a.psum + (size_t)router_balance_ctas(M) * E);
     }
     return launch_router_forward(a, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }

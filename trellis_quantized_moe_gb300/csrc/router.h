@@ -17,14 +17,30 @@ struct RouterArgs {
     const uint8_t *valid;
     int32_t *counts;
     float *loss;
-    float *mean;                    // workspace: f32 [E], mean probability of each expert
+    float *psum;                    // workspace: f32 [ctas][E], each CTA's sum of probabilities
+    int32_t *pcount;                // workspace: int32 [ctas][E + 1], its counts and valid rows
     // backward
     const void *d_rw;
     const float *d_loss;
     void *d_logits;
 };
 
+// CTAs of the balance pass at most: two of 16 warps per SM.
+constexpr int kRouterCtas = 304;
+constexpr int kRouterWarps = 16;
+// Balance of at most this many rows: one CTA does it all, with no second kernel.
+constexpr int kRouterOneCta = 64;
+
+inline int router_balance_ctas(int M)
+{
+    if (M <= kRouterOneCta)
+        return M > 0;
+    const int n = (M + kRouterWarps - 1) / kRouterWarps;
+    return n < kRouterCtas ? n : kRouterCtas;
+}
+
 size_t router_workspace_bytes(int M, int E);
+cudaError_t router_set_attributes();
 cudaError_t launch_router_forward(const RouterArgs &a, cudaStream_t s);
 cudaError_t launch_router_backward(const RouterArgs &a, cudaStream_t s);
 
