@@ -236,7 +236,7 @@ int exl3_linear_noalloc_error(int32_t *err_host, cudaStream_t stream);
  * Per row t: m_t = max_e l_te, s_t = sum_e exp(l_te - m_t), p_te =
  * exp(l_te - m_t) / s_t.  S_t = the
  * topk largest logits, descending, ties to the lower expert (-0 equals +0, a
- * NaN orders below -inf).  rw_tj = p at S_tj, or (renorm) that divided by the
+ * NaN orders as -inf).  rw_tj = p at S_tj, or (renorm) that divided by the
  * sum of p over S_t.  An expert of logit -inf has p = 0; a row of -inf only has
  * p = 0, rw = 0 and S = 0..topk-1; a row that holds a NaN or +inf has NaN
  * weights (its ids are still in [0, E)).

@@ -31,9 +31,7 @@ def oracle(z, k, renorm, valid=None, d_rw=None, d_loss=0.0):
     """ids, rw, stats, counts, loss, d_logits and the size of its terms, in float64."""
     M, E = z.shape
     key = np.where(np.isnan(z), -np.inf, z)
-    # NaN after -inf: sort by (is NaN, -logit), stable in the expert
-    ids = np.stack([np.lexsort((np.arange(E), -key[t], np.isnan(z[t])))[:k] for t in range(M)]) \
-        if M else np.zeros((0, k), int)
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :k]
     with np.errstate(invalid="ignore", divide="ignore"):
         m = np.max(z, axis=1, keepdims=True) if M else np.zeros((0, 1))
         ref = np.where(m == -np.inf, 0.0, m)

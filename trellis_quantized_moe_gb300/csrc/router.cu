@@ -5,15 +5,15 @@
 // registers, so the row is read once.  Forward: m = max l, s = sum exp(l - m),
 // p_e = exp(l_e - m) / s (kept as the pair: m + log s in fp32 would lose s for
 // large |m|); then topk rounds of a warp-wide maximum over order-preserving
-// integer keys, ties to the lower expert.  Backward, with G_e = dL/dp_e
+// integer keys, ties to the lower expert (Chooser).  Backward, with G_e = dL/dp_e
 // (balance term on valid rows, plus the route weights' gradient where they are
 // plain probabilities):
 //   dl_e = p_e (G_e - sum_j p_j G_j),
 // and renormalised weights w, which depend on the chosen logits only, add
 // w_i (d_i - sum_j w_j d_j) at the chosen experts.
 //
-// What bounds it: not HBM but the instructions of the topk rounds (about 30
-// per round and row at 192 experts).
+// What bounds it: not HBM but the instructions per row, most of them the
+// choice's.
 #include <type_traits>
 
 #include "common.cuh"
@@ -41,42 +41,132 @@ EXL3_DEV void store_float(void *p, size_t i, int dtype, float v)
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// Keys in the order of the logits, never 0 (0: no expert, or taken): NaN
-// lowest, then -inf .. +inf, with -0 and +0 equal.
+// A row of logits as it lies in memory, lane l: experts l + 32 i.
+template <int DT, int V>
+struct RawRow {
+    using T = std::conditional_t<DT == EXL3_F32, float, uint16_t>;
+    T v[V];
+    EXL3_DEV void load(const void *p, size_t row, int E)
+    {
+        const int lane = threadIdx.x & 31;
+        const T *q = static_cast<const T *>(p) + row + lane;
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            v[i] = lane + 32 * i < E ? q[32 * i] : T(0);
+    }
+    EXL3_DEV float get(int i) const
+    {
+        if constexpr (DT == EXL3_F32)
+            return v[i];
+        else if constexpr (DT == EXL3_BF16)
+            return __uint_as_float((uint32_t)v[i] << 16);
+        else
+            return __half2float(__ushort_as_half(v[i]));
+    }
+};
+
+// Unsigned integers in the order of the logits, -0 as +0 and NaN as -inf.
+// 16-bit logits (as fp32) order by their upper 19 bits: the lower 13 bits take
+// the complement of the expert, so that one integer maximum also settles ties.
 EXL3_DEV uint32_t order_key(float l)
 {
-    const uint32_t u = __float_as_uint(l + 0.0f);
-    const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-    return isnan(l) ? 1u : k;
+    const uint32_t u = __float_as_uint(fmaxf(l, -INFINITY) + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+EXL3_DEV float key_logit(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-EXL3_DEV float key_logit(uint32_t k)
+constexpr uint32_t kExpertBits = 0x1FFF;           // 13 bits; 1024 experts need 10
+
+// Batcher's merge exchange: sorts v[0..V) descending, with `swap` exchanging a
+// pair that is out of order.
+template <int V, typename Swap>
+EXL3_DEV void sort_network(Swap swap)
 {
-    return k == 1u ? __uint_as_float(0x7FC00000u)
-                   : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    constexpr int kP2 = V <= 1 ? 1 : V <= 2 ? 2 : V <= 4 ? 4 : V <= 8 ? 8 : V <= 16 ? 16 : 32;
+#pragma unroll
+    for (int p = 1; p < kP2; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < kP2; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; i++)
+                    if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+                        swap(i + j, i + j + k);
 }
 
-// A row's logits, lane l: experts l + 32 i (absent ones: `pad`).
+// The row's experts in order of choice, one call per round: every lane keeps
+// its own experts sorted (a network of V log^2 V exchanges on registers, no
+// branches) and shows the first; the owner of the warp's best moves up.
+template <bool PACKED, int V>
+struct Chooser;
+
 template <int V>
-EXL3_DEV void load_row(const void *p, size_t row, int E, int dtype, float pad, float (&v)[V])
-{
-    const int lane = threadIdx.x & 31;
-    if (dtype == EXL3_F32) {
+struct Chooser<true, V> {                          // 16-bit logits: expert in the key
+    uint32_t k[V];
+    EXL3_DEV void init(const float (&l)[V], int E)
+    {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = lane + 32 * i < E ? static_cast<const float *>(p)[row + lane + 32 * i] : pad;
-    } else if (dtype == EXL3_BF16) {
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = lane + 32 * i < E
-                       ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[row + lane + 32 * i])
-                       : pad;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = lane + 32 * i < E ? __half2float(static_cast<const __half *>(p)[row + lane + 32 * i]) : pad;
+        for (int i = 0; i < V; i++) {
+            const int e = lane + 32 * i;
+            k[i] = e < E ? (order_key(l[i]) & ~kExpertBits) | (kExpertBits - e) : 0u;
+        }
+        sort_network<V>([&](int a, int b) {
+            const uint32_t hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+            k[a] = hi;
+            k[b] = lo;
+        });
     }
-}
+    EXL3_DEV void next(uint32_t &key, int &expert)
+    {
+        const uint32_t b = __reduce_max_sync(0xffffffffu, k[0]);
+        const bool own = k[0] == b;
+#pragma unroll
+        for (int i = 0; i + 1 < V; i++)
+            k[i] = own ? k[i + 1] : k[i];
+        k[V - 1] = own ? 0u : k[V - 1];
+        expert = kExpertBits - (b & kExpertBits);
+        // a negative logit's key has ones where the fraction ends
+        key = b & 0x80000000u ? b & ~kExpertBits : b | kExpertBits;
+    }
+};
+
+template <int V>
+struct Chooser<false, V> {                         // fp32 logits: key and expert side by side
+    uint32_t k[V];
+    int e[V];
+    EXL3_DEV void init(const float (&l)[V], int E)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            e[i] = lane + 32 * i;
+            k[i] = e[i] < E ? order_key(l[i]) : 0u;           // every logit's key is above 0
+        }
+        sort_network<V>([&](int a, int b) {
+            const bool x = k[a] < k[b] || (k[a] == k[b] && e[a] > e[b]);
+            const uint32_t ka = k[a];
+            const int ea = e[a];
+            k[a] = x ? k[b] : ka;
+            e[a] = x ? e[b] : ea;
+            k[b] = x ? ka : k[b];
+            e[b] = x ? ea : e[b];
+        });
+    }
+    EXL3_DEV void next(uint32_t &key, int &expert)
+    {
+        key = __reduce_max_sync(0xffffffffu, k[0]);
+        expert = __reduce_min_sync(0xffffffffu, k[0] == key ? e[0] : 0x7FFFFFFF);
+        const bool own = e[0] == expert && k[0] == key;
+#pragma unroll
+        for (int i = 0; i + 1 < V; i++) {
+            k[i] = own ? k[i + 1] : k[i];
+            e[i] = own ? e[i + 1] : e[i];
+        }
+        k[V - 1] = own ? 0u : k[V - 1];
+    }
+};
 
 // counts, T and loss from one expert's totals per thread: thread e of the CTA
 // holds c and p of expert e0 + e; returns the CTA's part of sum c_e p_e in
@@ -104,7 +194,7 @@ EXL3_DEV float loss_of(const RouterArgs &a, float dot, int T)
 // V: experts per lane.  BAL: counts and probability sums as well; each CTA
 // leaves its own in the workspace (rows are dealt to warps in a fixed way and
 // everything is added in a fixed order), or finishes alone (one CTA).
-template <int V, bool BAL>
+template <int DT, int V, bool BAL>
 __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs a)
 {
     extern __shared__ float sm[];                  // BAL: [E + 1] counts, then [warps][E] sums
@@ -123,22 +213,26 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
             psum[i] = 0.0f;
         __syncthreads();
     }
-    for (int t = blockIdx.x * nw + warp; t < a.M; t += gridDim.x * nw) {
+    const int step = gridDim.x * nw;
+    RawRow<DT, V> raw;
+    int t = blockIdx.x * nw + warp;
+    if (t < a.M)
+        raw.load(a.logits, (size_t)t * E, E);
+    for (; t < a.M; t += step) {
         float l[V];
-        load_row<V>(a.logits, (size_t)t * E, E, a.logits_dtype, -INFINITY, l);
-        uint32_t key[V], best = 0;
-        int slot = 0;
 #pragma unroll
-        for (int i = V - 1; i >= 0; i--) {
-            key[i] = lane + 32 * i < E ? order_key(l[i]) : 0u;
-            if (key[i] >= best) {
-                best = key[i];
-                slot = i;
-            }
-        }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const float m = key_logit(top);
-        const float ref = m == -INFINITY ? 0.0f : m;           // NaN where every logit is NaN
+        for (int i = 0; i < V; i++)
+            l[i] = lane + 32 * i < E ? raw.get(i) : -INFINITY;
+        const bool ok = BAL && (!a.valid || a.valid[t] != 0);
+        if (t + step < a.M)                        // the next row, one round of work ahead
+            raw.load(a.logits, (size_t)(t + step) * E, E);
+        Chooser<DT != EXL3_F32, V> choose;
+        choose.init(l, E);
+        uint32_t mine;
+        int id;
+        choose.next(mine, id);                     // the first choice has the largest logit
+        const float m = key_logit(mine);
+        const float ref = m == -INFINITY ? 0.0f : m;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) {
@@ -149,39 +243,18 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
         const float inv = s == 0.0f ? 0.0f : 1.0f / s;
         if (a.stats && lane == 0)
             reinterpret_cast<float2 *>(a.stats)[t] = make_float2(ref, s);
-        bool ok = false;
-        if (BAL) {
-            ok = !a.valid || a.valid[t] != 0;
-            if (ok) {
-                nvalid++;
+        if (ok) {
+            nvalid++;
 #pragma unroll
-                for (int i = 0; i < V; i++)
-                    psum[i] += l[i] * inv;
-            }
+            for (int i = 0; i < V; i++)
+                psum[i] = fmaf(l[i], inv, psum[i]);
         }
-        // round j: the warp's best key, the lowest expert that has it; lane j
-        // keeps the pair, the owner drops it
-        uint32_t mine = 0;
-        int id = 0;
-        for (int j = 0; j < k; j++) {
-            const uint32_t b = j == 0 ? top : __reduce_max_sync(0xffffffffu, best);
-            const int e = __reduce_min_sync(0xffffffffu, best == b ? slot * 32 + lane : 0x7FFFFFFF);
-            if (lane == j) {
-                mine = b;
-                id = e;
-            }
-            if (lane == (e & 31)) {
-                const int out = e >> 5;
-                best = 0;
-#pragma unroll
-                for (int i = V - 1; i >= 0; i--) {
-                    key[i] = i == out ? 0u : key[i];
-                    if (key[i] >= best) {
-                        best = key[i];
-                        slot = i;
-                    }
-                }
-            }
+        for (int j = 1; j < k; j++) {              // lane j keeps round j's choice
+            uint32_t b;
+            int e;
+            choose.next(b, e);
+            mine = lane == j ? b : mine;
+            id = lane == j ? e : id;
         }
         float w = lane < k ? __expf(key_logit(mine) - ref) * inv : 0.0f;
         if (a.renorm) {
@@ -242,18 +315,18 @@ EXL3_DEV void cluster_sync()
 __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_router_join(RouterArgs a, int n)
 {
     __shared__ float sp[kJoinThreads], scratch[32], parts[kJoin];
-    __shared__ int sc[kJoinThreads], T;
+    __shared__ int sc[kJoinThreads];
     const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     cluster_sync();                                // CTA 0's shared memory may be written from here on
     grid_dep_wait();
-    if (warp == 0) {
-        int t = 0;
-        for (int g = lane; g < n; g += 32)
-            t += a.pcount[(size_t)g * (E + 1) + E];
-        t = __reduce_add_sync(0xffffffffu, t);
-        if (lane == 0)
-            T = t;
-    }
+    // valid rows: a thread per CTA of the balance pass
+    int t = threadIdx.x < n ? a.pcount[(size_t)threadIdx.x * (E + 1) + E] : 0;
+    t = __reduce_add_sync(0xffffffffu, t);
+    if (lane == 0)
+        sc[warp] = t;
+    __syncthreads();
+    const int T = __reduce_add_sync(0xffffffffu, sc[lane]);
+    __syncthreads();
     const int per = (E + kJoin - 1) / kJoin, e0 = blockIdx.x * per, e1 = min(E, e0 + per);
     float dot = 0.0f;
     for (int base = e0; base < e1; base += 32) {   // 32 experts at a time, 32 threads each
@@ -298,7 +371,7 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
 
 constexpr int kBackWarps = 8;
 
-template <int V>
+template <int DT, int V>
 __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs a)
 {
     extern __shared__ float sm[];                  // [warps][E]: the row's gradients at chosen experts
@@ -319,63 +392,91 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
         for (int i = 0; i < V; i++)
             g[i] = a.counts && lane + 32 * i < E ? cg * (float)a.counts[lane + 32 * i] : 0.0f;
     }
-    for (int t = blockIdx.x * kBackWarps + warp; t < a.M; t += gridDim.x * kBackWarps) {
-        const size_t row = (size_t)t * E;
-        const float2 st = reinterpret_cast<const float2 *>(a.stats)[t];
-        const float inv = st.y == 0.0f ? 0.0f : 1.0f / st.y;
-        const bool bal = a.counts && (!a.valid || a.valid[t] != 0);
-        int id = -1;
-        float d = 0.0f, pj = 0.0f;
+    // one row's inputs, read a row ahead of their use
+    struct Row {
+        RawRow<DT, V> raw;
+        float2 st;
+        float d, chosen;
+        int id;
+        bool bal;
+    } next;
+    auto fetch = [&](int t, Row &r) {
+        r.raw.load(a.logits, (size_t)t * E, E);
+        r.st = reinterpret_cast<const float2 *>(a.stats)[t];
+        r.bal = a.counts && (!a.valid || a.valid[t] != 0);
+        r.id = -1;
+        r.d = r.chosen = 0.0f;
         if (a.d_rw && lane < k) {
-            id = a.ids[(size_t)t * k + lane];
-            d = load_act(a.d_rw, (size_t)t * k + lane, a.rw_dtype);
-            if ((unsigned)id >= (unsigned)E)
-                id = -1;
+            r.id = a.ids[(size_t)t * k + lane];
+            r.d = load_act(a.d_rw, (size_t)t * k + lane, a.rw_dtype);
+            if ((unsigned)r.id >= (unsigned)E)
+                r.id = -1;
+            else if (a.renorm)
+                r.chosen = load_act(a.logits, (size_t)t * E + r.id, DT);
         }
-        float p[V];
-        load_row<V>(a.logits, row, E, a.logits_dtype, -INFINITY, p);
+    };
+    const int step = gridDim.x * kBackWarps;
+    int t = blockIdx.x * kBackWarps + warp;
+    if (t < a.M)
+        fetch(t, next);
+    for (; t < a.M; t += step) {
+        const Row r = next;
+        if (t + step < a.M)
+            fetch(t + step, next);
+        const float inv = r.st.y == 0.0f ? 0.0f : 1.0f / r.st.y;
+        const bool some = r.st.y != 0.0f;
         if (a.d_rw) {
-            float add = d;
+            float add = r.d;
             if (a.renorm) {                        // w_j (d_j - sum w d), beside the softmax's own term
-                pj = id >= 0 ? __expf(load_act(a.logits, row + id, a.logits_dtype) - st.x) * inv : 0.0f;
+                const float pj = r.id >= 0 && some ? __expf(r.chosen - r.st.x) * inv : 0.0f;
                 const float total = warp_sum(pj);
                 const float w = total == 0.0f ? 0.0f : pj / total;
-                const float wd = warp_sum(id >= 0 ? w * d : 0.0f);
-                add = w * (d - wd);
+                const float wd = warp_sum(r.id >= 0 ? w * r.d : 0.0f);
+                add = w * (r.d - wd);
             }
-            if (id >= 0)
-                atomicAdd(at + id, add);           // distinct ids: one addend each
+            if (r.id >= 0)
+                atomicAdd(at + r.id, add);         // distinct ids: one addend each
             __syncwarp();
         }
-        float pg = 0.0f;
+        float p[V], own[V], pg = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            p[i] = inv == 0.0f ? 0.0f : __expf(p[i] - st.x) * inv;
-            float G = bal ? g[i] : 0.0f;
-            if (a.d_rw && !a.renorm && lane + 32 * i < E)
-                G += at[lane + 32 * i];
-            pg = fmaf(p[i], G, pg);
+            p[i] = some ? __expf(r.raw.get(i) - r.st.x) * inv : 0.0f;
+            own[i] = a.d_rw && lane + 32 * i < E ? at[lane + 32 * i] : 0.0f;
         }
-        pg = warp_sum(pg);
+        if (a.renorm) {
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int e = lane + 32 * i;
-            if (e < E) {
-                const float own = a.d_rw ? at[e] : 0.0f;
-                const float G = (bal ? g[i] : 0.0f) + (a.renorm ? 0.0f : own);
-                store_float(a.d_logits, row + e, a.logits_dtype, fmaf(p[i], G - pg, a.renorm ? own : 0.0f));
+            for (int i = 0; i < V; i++)
+                pg = lane + 32 * i < E && r.bal ? fmaf(p[i], g[i], pg) : pg;
+            pg = warp_sum(pg);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                own[i] = fmaf(p[i], (r.bal ? g[i] : 0.0f) - pg, own[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                own[i] += r.bal ? g[i] : 0.0f;
+                pg = lane + 32 * i < E ? fmaf(p[i], own[i], pg) : pg;
             }
+            pg = warp_sum(pg);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                own[i] = p[i] * (own[i] - pg);
         }
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            if (lane + 32 * i < E)
+                store_float(a.d_logits, (size_t)t * E + lane + 32 * i, DT, own[i]);
         if (a.d_rw) {
             __syncwarp();
-            if (id >= 0)
-                at[id] = 0.0f;
+            if (r.id >= 0)
+                at[r.id] = 0.0f;
             __syncwarp();
         }
     }
 }
 
-template <int V>
+template <int DT, int V>
 cudaError_t forward(const RouterArgs &a, cudaStream_t s)
 {
     const size_t bal_smem = ((size_t)a.E + 1 + (size_t)kRouterWarps * a.E) * 4;
@@ -383,12 +484,12 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
         // few rows: a warp each on as many SMs as there are
         const int warps = a.M >= a.num_sms * kRouterWarps ? kRouterWarps : a.M >= 4 * a.num_sms ? 4 : 1;
         const int need = (a.M + warps - 1) / warps, most = a.num_sms * (64 / kRouterWarps) * (kRouterWarps / warps);
-        k_router_forward<V, false><<<need < most ? need : most, warps * 32, 0, s>>>(a);
+        k_router_forward<DT, V, false><<<need < most ? need : most, warps * 32, 0, s>>>(a);
         return cudaGetLastError();
     }
     const int n = router_balance_ctas(a.M);
     if (n > 0)
-        k_router_forward<V, true><<<n, kRouterWarps * 32, bal_smem, s>>>(a);
+        k_router_forward<DT, V, true><<<n, kRouterWarps * 32, bal_smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (n == 1 || e != cudaSuccess)
         return e;
@@ -404,28 +505,38 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, k_router_join, a, n);
 }
 
-template <int V>
+template <int DT, int V>
 cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
     const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 8;
-    k_router_backward<V><<<need < most ? need : most, kBackWarps * 32, (size_t)kBackWarps * a.E * 4, s>>>(a);
+    k_router_backward<DT, V>
+        <<<need < most ? need : most, kBackWarps * 32, (size_t)kBackWarps * a.E * 4, s>>>(a);
     return cudaGetLastError();
 }
 
-// The smallest instantiation that holds E experts.
-template <typename F>
+// f(dtype, experts per lane) for the smallest instantiation that holds E experts.
+template <int DT, typename F>
 cudaError_t by_width(int E, F f)
 {
+    constexpr std::integral_constant<int, DT> dt;
     const int v = (E + 31) / 32;
-    if (v <= 1) return f(std::integral_constant<int, 1>());
-    if (v <= 2) return f(std::integral_constant<int, 2>());
-    if (v <= 4) return f(std::integral_constant<int, 4>());
-    if (v <= 6) return f(std::integral_constant<int, 6>());
-    if (v <= 8) return f(std::integral_constant<int, 8>());
-    if (v <= 10) return f(std::integral_constant<int, 10>());
-    if (v <= 12) return f(std::integral_constant<int, 12>());
-    if (v <= 16) return f(std::integral_constant<int, 16>());
-    return f(std::integral_constant<int, 32>());
+    if (v <= 1) return f(dt, std::integral_constant<int, 1>());
+    if (v <= 2) return f(dt, std::integral_constant<int, 2>());
+    if (v <= 4) return f(dt, std::integral_constant<int, 4>());
+    if (v <= 6) return f(dt, std::integral_constant<int, 6>());
+    if (v <= 8) return f(dt, std::integral_constant<int, 8>());
+    if (v <= 10) return f(dt, std::integral_constant<int, 10>());
+    if (v <= 12) return f(dt, std::integral_constant<int, 12>());
+    if (v <= 16) return f(dt, std::integral_constant<int, 16>());
+    return f(dt, std::integral_constant<int, 32>());
+}
+
+template <typename F>
+cudaError_t by_row(int dtype, int E, F f)
+{
+    return dtype == EXL3_F32    ? by_width<EXL3_F32>(E, f)
+           : dtype == EXL3_BF16 ? by_width<EXL3_BF16>(E, f)
+                                : by_width<EXL3_F16>(E, f);
 }
 
 }  // namespace
@@ -433,8 +544,12 @@ cudaError_t by_width(int E, F f)
 // The balance pass of more than 512 experts needs more than 48 KB of sums.
 cudaError_t router_set_attributes()
 {
-    return cudaFuncSetAttribute(k_router_forward<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (EXL3_MAX_EXPERTS * (kRouterWarps + 1) + 1) * 4);
+    const int most = (EXL3_MAX_EXPERTS * (kRouterWarps + 1) + 1) * 4;
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(k_router_forward<EXL3_F32, 32, true>, attr, most);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_router_forward<EXL3_BF16, 32, true>, attr, most);
+    return e == cudaSuccess ? cudaFuncSetAttribute(k_router_forward<EXL3_F16, 32, true>, attr, most) : e;
 }
 
 size_t router_workspace_bytes(int M, int E)
@@ -447,12 +562,12 @@ cudaError_t launch_router_forward(const RouterArgs &a, cudaStream_t s)
 {
     if (a.M == 0 && !a.counts)
         return cudaSuccess;
-    return by_width(a.E, [&](auto v) { return forward<v.value>(a, s); });
+    return by_row(a.logits_dtype, a.E, [&](auto dt, auto v) { return forward<dt.value, v.value>(a, s); });
 }
 
 cudaError_t launch_router_backward(const RouterArgs &a, cudaStream_t s)
 {
-    return by_width(a.E, [&](auto v) { return backward<v.value>(a, s); });
+    return by_row(a.logits_dtype, a.E, [&](auto dt, auto v) { return backward<dt.value, v.value>(a, s); });
 }
 
 }  // namespace exl3
