@@ -118,7 +118,8 @@ struct Chooser<true, V> {                          // 16-bit logits: expert in t
             k[b] = lo;
         });
     }
-    EXL3_DEV void next(uint32_t &key, int &expert)
+    // this round's choice, kept by lane j
+    EXL3_DEV void next(int j, uint32_t &mine, int &)
     {
         const uint32_t b = __reduce_max_sync(0xffffffffu, k[0]);
         const bool own = k[0] == b;
@@ -126,10 +127,11 @@ struct Chooser<true, V> {                          // 16-bit logits: expert in t
         for (int i = 0; i + 1 < V; i++)
             k[i] = own ? k[i + 1] : k[i];
         k[V - 1] = own ? 0u : k[V - 1];
-        expert = kExpertBits - (b & kExpertBits);
-        // a negative logit's key has ones where the fraction ends
-        key = b & 0x80000000u ? b & ~kExpertBits : b | kExpertBits;
+        mine = (threadIdx.x & 31) == j ? b : mine;
     }
+    // a negative logit's key has ones where the fraction ends
+    static EXL3_DEV uint32_t key(uint32_t b) { return b & 0x80000000u ? b & ~kExpertBits : b | kExpertBits; }
+    static EXL3_DEV int expert(uint32_t b, int) { return kExpertBits - (b & kExpertBits); }
 };
 
 template <int V>
@@ -154,11 +156,13 @@ struct Chooser<false, V> {                         // fp32 logits: key and exper
             e[b] = x ? ea : e[b];
         });
     }
-    EXL3_DEV void next(uint32_t &key, int &expert)
+    EXL3_DEV void next(int j, uint32_t &mine, int &id)
     {
-        key = __reduce_max_sync(0xffffffffu, k[0]);
-        expert = __reduce_min_sync(0xffffffffu, k[0] == key ? e[0] : 0x7FFFFFFF);
-        const bool own = e[0] == expert && k[0] == key;
+        const uint32_t b = __reduce_max_sync(0xffffffffu, k[0]);
+        const int x = __reduce_min_sync(0xffffffffu, k[0] == b ? e[0] : 0x7FFFFFFF);
+        const bool own = e[0] == x && k[0] == b;
+        mine = (threadIdx.x & 31) == j ? b : mine;
+        id = (threadIdx.x & 31) == j ? x : id;
 #pragma unroll
         for (int i = 0; i + 1 < V; i++) {
             k[i] = own ? k[i + 1] : k[i];
@@ -166,6 +170,8 @@ struct Chooser<false, V> {                         // fp32 logits: key and exper
         }
         k[V - 1] = own ? 0u : k[V - 1];
     }
+    static EXL3_DEV uint32_t key(uint32_t b) { return b; }
+    static EXL3_DEV int expert(uint32_t, int id) { return id; }
 };
 
 // counts, T and loss from one expert's totals per thread: thread e of the CTA
@@ -226,12 +232,13 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
         const bool ok = BAL && (!a.valid || a.valid[t] != 0);
         if (t + step < a.M)                        // the next row, one round of work ahead
             raw.load(a.logits, (size_t)(t + step) * E, E);
-        Chooser<DT != EXL3_F32, V> choose;
+        using C = Chooser<DT != EXL3_F32, V>;
+        C choose;
         choose.init(l, E);
-        uint32_t mine;
-        int id;
-        choose.next(mine, id);                     // the first choice has the largest logit
-        const float m = key_logit(mine);
+        uint32_t mine = 0;
+        int id = 0;
+        choose.next(0, mine, id);                  // the first choice has the largest logit
+        const float m = key_logit(C::key(__shfl_sync(0xffffffffu, mine, 0)));
         const float ref = m == -INFINITY ? 0.0f : m;
         float s = 0.0f;
 #pragma unroll
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
             s += l[i];
         }
         s = warp_sum(s);
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);    // s is 0 or in [1, E]
         if (a.stats && lane == 0)
             reinterpret_cast<float2 *>(a.stats)[t] = make_float2(ref, s);
         if (ok) {
@@ -249,14 +256,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
             for (int i = 0; i < V; i++)
                 psum[i] = fmaf(l[i], inv, psum[i]);
         }
-        for (int j = 1; j < k; j++) {              // lane j keeps round j's choice
-            uint32_t b;
-            int e;
-            choose.next(b, e);
-            mine = lane == j ? b : mine;
-            id = lane == j ? e : id;
-        }
-        float w = lane < k ? __expf(key_logit(mine) - ref) * inv : 0.0f;
+        for (int j = 1; j < k; j++)
+            choose.next(j, mine, id);
+        id = C::expert(mine, id);
+        float w = lane < k ? __expf(key_logit(C::key(mine)) - ref) * inv : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(w);
             w = total == 0.0f ? 0.0f : w / total;
@@ -333,12 +336,22 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
         const int e = base + lane;
         float p = 0.0f;
         int c = 0;
-        if (e < e1)
-#pragma unroll 10
-            for (int g = warp; g < n; g += 32) {
-                p += a.psum[(size_t)g * E + e];
-                c += a.pcount[(size_t)g * (E + 1) + e];
-            }
+        // every load in flight at once: a loop with a remainder took 10 us here
+        constexpr int kMost = (kRouterCtas + 31) / 32;
+        float lp[kMost];
+        int lc[kMost];
+#pragma unroll
+        for (int u = 0; u < kMost; u++) {
+            const int g = warp + 32 * u;
+            const bool in = e < e1 && g < n;
+            lp[u] = in ? a.psum[(size_t)g * E + e] : 0.0f;
+            lc[u] = in ? a.pcount[(size_t)g * (E + 1) + e] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kMost; u++) {
+            p += lp[u];
+            c += lc[u];
+        }
         sp[threadIdx.x] = p;
         sc[threadIdx.x] = c;
         __syncthreads();
@@ -423,7 +436,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
         const Row r = next;
         if (t + step < a.M)
             fetch(t + step, next);
-        const float inv = r.st.y == 0.0f ? 0.0f : 1.0f / r.st.y;
+        const float inv = r.st.y == 0.0f ? 0.0f : __fdividef(1.0f, r.st.y);
         const bool some = r.st.y != 0.0f;
         if (a.d_rw) {
             float add = r.d;
