@@ -46,42 +46,87 @@ int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, 
 // One CTA per SM shares a product's work; the workspace knows kLoraCtas of them.
 int product_ctas(int sms) { return sms < kLoraCtas ? sms : kLoraCtas; }
 
-LoraShrinkArgs shrink_args(int act_dtype, int M, const exl3_adapters *ad, const exl3_adapters *grads,
-                           const void *plan, void *ws, const LoraWsLayout &L)
-{
-    LoraShrinkArgs a{};
-    a.plan = static_cast<const int32_t *>(plan);
-    a.M = M;
-    a.N = ad->N;
-    a.act_dtype = act_dtype;
-    a.max_rank = ad->max_rank;
-    a.h_cols = lora_h_cols(ad->max_rank);
-    a.rank = ad->rank;
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
-    a.A = ad->A;
-    a.B = ad->B;
-    a.GA = grads ? grads->A : nullptr;
-    a.GB = grads ? grads->B : nullptr;
-    a.hdr = static_cast<int32_t *>(ws);
-    return a;
-}
+// Rows up to which one launch does both products: above, the products' own
+// kernels read each weight once per 128 rows instead of once per 16.
+constexpr int kRowsMax = 128;
 
-// The expand that follows shrink `sh`, launched with `ctas` CTAs.
-LoraExpandArgs expand_args(const LoraShrinkArgs &sh, const exl3_adapters *ad, int ctas)
+// h = h_scale * W1 x, y = base + y_scale * h W2 of a batch (scale_h: the
+// adapter's scale goes to h instead of y), and the check of the tables.
+struct Products {
+    const void *x;
+    const int64_t *W1, *W2;
+    int in_width, out_width, scale_h;
+    const void *base;
+    void *y, *h;
+};
+
+cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_adapters *ad,
+                         const exl3_adapters *grads, const void *plan, void *ws, const LoraWsLayout &L, int ctas,
+                         cudaStream_t stream)
 {
-    LoraExpandArgs a{};
-    a.plan = sh.plan;
-    a.M = sh.M;
-    a.N = sh.N;
-    a.act_dtype = sh.act_dtype;
-    a.h_cols = sh.h_cols;
-    a.part = sh.part;
-    a.shrink_width = sh.width;
-    a.shrink_ctas = ctas;
-    a.rank = ad->rank;
-    a.scale = ad->scale;
-    a.hdr = sh.hdr;
-    return a;
+    if (M <= kRowsMax) {
+        LoraRowsArgs a{};
+        a.plan = static_cast<const int32_t *>(plan);
+        a.M = M;
+        a.N = ad->N;
+        a.act_dtype = act_dtype;
+        a.max_rank = ad->max_rank;
+        a.h_cols = lora_h_cols(ad->max_rank);
+        a.in_width = p.in_width;
+        a.out_width = p.out_width;
+        a.scale_h = p.scale_h;
+        a.x = p.x;
+        a.W1 = p.W1;
+        a.W2 = p.W2;
+        a.GA = grads ? grads->A : nullptr;
+        a.GB = grads ? grads->B : nullptr;
+        a.rank = ad->rank;
+        a.scale = ad->scale;
+        a.base = p.base;
+        a.y = p.y;
+        a.h = p.h;
+        a.hdr = static_cast<int32_t *>(ws);
+        return launch_lora_rows(a, stream);
+    }
+    LoraShrinkArgs sh{};
+    sh.plan = static_cast<const int32_t *>(plan);
+    sh.M = M;
+    sh.N = ad->N;
+    sh.act_dtype = act_dtype;
+    sh.max_rank = ad->max_rank;
+    sh.h_cols = lora_h_cols(ad->max_rank);
+    sh.width = p.in_width;
+    sh.x = p.x;
+    sh.W = p.W1;
+    sh.rank = ad->rank;
+    sh.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
+    sh.A = ad->A;
+    sh.B = ad->B;
+    sh.GA = grads ? grads->A : nullptr;
+    sh.GB = grads ? grads->B : nullptr;
+    sh.hdr = static_cast<int32_t *>(ws);
+    const cudaError_t e = launch_lora_shrink(sh, ctas, stream);
+    if (e != cudaSuccess)
+        return e;
+    LoraExpandArgs ex{};
+    ex.plan = sh.plan;
+    ex.M = M;
+    ex.N = sh.N;
+    ex.act_dtype = act_dtype;
+    ex.h_cols = sh.h_cols;
+    ex.width = p.out_width;
+    ex.scale_h = p.scale_h;
+    ex.part = sh.part;
+    ex.shrink_width = sh.width;
+    ex.shrink_ctas = ctas;
+    ex.h = p.h;
+    ex.W = p.W2;
+    ex.rank = ad->rank;
+    ex.scale = ad->scale;
+    ex.base = p.base;
+    ex.y = p.y;
+    ex.hdr = sh.hdr;
+    return launch_lora_expand(ex, ctas, stream);
 }
 
 }  // namespace
@@ -153,20 +198,10 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
     if (M == 0)
         return EXL3_OK;
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
-    const int ctas = product_ctas(sms);
-    LoraShrinkArgs sh = shrink_args(act_dtype, M, ad, nullptr, plan, ws, L);
-    sh.x = x;
-    sh.W = ad->A;
-    sh.width = ad->in_features;
-    LoraExpandArgs ex = expand_args(sh, ad, ctas);
-    ex.h = h;
-    ex.W = ad->B;
-    ex.width = ad->out_features;
-    ex.base = base;
-    ex.y = y;
-    if (launch_lora_shrink(sh, ctas, stream) != cudaSuccess)
-        return EXL3_E_CUDA;
-    return launch_lora_expand(ex, ctas, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
+    const Products p{x, ad->A, ad->B, ad->in_features, ad->out_features, 0, base, y, h};
+    return run_products(p, act_dtype, M, ad, nullptr, plan, ws, L, product_ctas(sms), stream) == cudaSuccess
+               ? EXL3_OK
+               : EXL3_E_CUDA;
 }
 
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
@@ -202,36 +237,24 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
     const int ctas = product_ctas(sms);
     void *dh = static_cast<uint8_t *>(ws) + L.h;
-    LoraShrinkArgs sh = shrink_args(act_dtype, M, ad, grads, plan, ws, L);
-    sh.x = dy;
-    sh.W = ad->B;
-    sh.width = ad->out_features;
-    LoraExpandArgs ex = expand_args(sh, ad, ctas);
-    ex.scale_h = 1;
-    ex.h = grads ? dh : nullptr;
-    ex.W = ad->A;
-    ex.width = ad->in_features;
-    ex.base = dx_base;
-    ex.y = dx;
-    if (launch_lora_shrink(sh, ctas, stream) != cudaSuccess)
-        return EXL3_E_CUDA;
-    if (M > 0 && launch_lora_expand(ex, ctas, stream) != cudaSuccess)
+    const Products p{dy, ad->B, ad->A, ad->out_features, ad->in_features, 1, dx_base, dx, grads ? dh : nullptr};
+    if (run_products(p, act_dtype, M, ad, grads, plan, ws, L, ctas, stream) != cudaSuccess)
         return EXL3_E_CUDA;
     if (!grads)
         return EXL3_OK;
     LoraOuterArgs o{};
-    o.plan = sh.plan;
+    o.plan = static_cast<const int32_t *>(plan);
     o.M = M;
-    o.N = sh.N;
+    o.N = ad->N;
     o.act_dtype = act_dtype;
-    o.h_cols = sh.h_cols;
+    o.h_cols = lora_h_cols(ad->max_rank);
     o.ctas = ctas;
     o.rank = ad->rank;
     o.scale = ad->scale;
     o.p[0] = {x, dh, grads->A, ad->in_features, 0};
     o.p[1] = {dy, h, grads->B, ad->out_features, 1};
-    o.part = sh.part;
-    o.hdr = sh.hdr;
+    o.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
+    o.hdr = static_cast<int32_t *>(ws);
     return launch_lora_outer(o, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }
 

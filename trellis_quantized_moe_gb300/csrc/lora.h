@@ -125,6 +125,20 @@ struct LoraExpandArgs {
     int32_t *hdr;
 };
 
+// rows: both products of a batch of few rows (and the table check) in one
+// launch: h = h_scale * W1 x, y = base + y_scale * h W2.
+struct LoraRowsArgs {
+    const int32_t *plan;
+    int M, N, act_dtype, max_rank, h_cols, in_width, out_width, scale_h;
+    const void *x;
+    const int64_t *W1, *W2, *GA, *GB;
+    const int32_t *rank;
+    const float *scale;
+    const void *base;
+    void *y, *h;
+    int32_t *hdr;
+};
+
 // outer: G_a[j][n] = g_scale * sum_s h[s][j] x[perm[s]][n], two such products
 // (dA and dB) in one launch; g_scale: the adapter's scale where `scaled`.
 struct LoraOuterArgs {
@@ -145,10 +159,12 @@ cudaError_t lora_set_attributes();
 cudaError_t launch_lora_plan(const LoraPlanArgs &a, int ids_dtype, cudaStream_t s);
 cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
+cudaError_t launch_lora_rows(const LoraRowsArgs &a, cudaStream_t s);
 cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);
 cudaError_t lora_plan_set_attributes();
 cudaError_t lora_shrink_set_attributes();
 cudaError_t lora_expand_set_attributes();
 cudaError_t lora_outer_set_attributes();
+cudaError_t lora_rows_set_attributes();
 
 }  // namespace exl3
