@@ -318,8 +318,8 @@ size_t exl3_lora_workspace_bytes(int M, int N, int in_features, int out_features
  *   act_dtype (f16/bf16).  h: act_dtype [M][exl3_lora_h_cols(max_rank)] or
  *   NULL: what the backward pass needs, rows in plan order. */
 int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *ad,
-                      const void *plan, const void *base, void *y, void *h, void *workspace,
-                      size_t ws_bytes, cudaStream_t stream);
+                      const void *plan, size_t plan_bytes, const void *base, void *y, void *h,
+                      void *workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* dy: [M][out]; x, h: of the forward pass.  dx: [M][in] or NULL (not wanted);
  *   dx_base: [M][in] or NULL (zero), may be dx.  grads: tables like ad's (its
@@ -328,7 +328,8 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
  *   written, zeros for one without rows.  At least one of dx, grads is needed.
  *   Sums over rows run in a fixed order: the same call gives the same bits. */
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
-                       const exl3_adapters *ad, const void *plan, const void *dx_base, void *dx,
+                       const exl3_adapters *ad, const void *plan, size_t plan_bytes,
+                       const void *dx_base, void *dx,
                        const exl3_adapters *grads, void *workspace, size_t ws_bytes,
                        cudaStream_t stream);
 

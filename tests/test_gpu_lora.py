@@ -161,7 +161,7 @@ def test_plan_is_the_stable_grouping(M, N, id64):
     key = np.where(b.ids_np < 0, N, b.ids_np)
     assert hdr[0] == 0 and np.array_equal(perm, np.argsort(key, kind="stable"))
     assert np.array_equal(off, np.concatenate([[0], np.cumsum(np.bincount(key, minlength=N + 1))]))
-    for t, size in ((tiles, 128), (small, 16)):
+    for t, size in ((tiles, 128), (small, 8)):
         want = [(a if a < N else -1, s, min(size, off[a + 1] - s), 0) for a in range(N + 1)
                 for s in range(off[a], off[a + 1], size)]
         assert np.array_equal(t, np.array(want, np.int32).reshape(-1, 4))

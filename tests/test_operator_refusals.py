@@ -91,13 +91,13 @@ _WSB = 1 << 40
 
 
 def _lf(ad=None, **kw):
-    d = dict(x=P, dt=1, M=4, ad=ctypes.byref(_ad(**(ad or {}))), plan=P, base=P, y=P, h=P, ws=P, wsb=_WSB)
+    d = dict(x=P, dt=1, M=4, ad=ctypes.byref(_ad(**(ad or {}))), plan=P, pb=_WSB, base=P, y=P, h=P, ws=P, wsb=_WSB)
     d.update(kw)
     return B.lib().exl3_lora_forward(*d.values(), None)
 
 
 def _lb(ad=None, grads=None, **kw):
-    d = dict(dy=P, x=P, h=P, dt=1, M=4, ad=ctypes.byref(_ad(**(ad or {}))), plan=P, dxb=P, dx=P,
+    d = dict(dy=P, x=P, h=P, dt=1, M=4, ad=ctypes.byref(_ad(**(ad or {}))), plan=P, pb=_WSB, dxb=P, dx=P,
              g=ctypes.byref(_ad(**(grads or {}))), ws=P, wsb=_WSB)
     d.update(kw)
     return B.lib().exl3_lora_backward(*d.values(), None)
@@ -112,7 +112,7 @@ def _lb(ad=None, grads=None, **kw):
     (dict(ad=dict(max_rank=129)), SHAPE), (dict(ad=dict(in_features=200)), SHAPE),
     (dict(ad=dict(out_features=0)), SHAPE), (dict(ad=dict(A=P + 4)), ALIGN),
     (dict(ad=dict(rank=P + 2)), ALIGN), (dict(plan=P + 16), ALIGN), (dict(ws=P + 128), ALIGN),
-    (dict(x=P + 8), ALIGN), (dict(h=P + 2), ALIGN), (dict(wsb=64), WORKSPACE),
+    (dict(x=P + 8), ALIGN), (dict(h=P + 2), ALIGN), (dict(wsb=64), WORKSPACE), (dict(pb=64), WORKSPACE),
 ])
 def test_adapter_calls_refuse(call, kw, code):
     assert call(**kw) == code
@@ -120,7 +120,7 @@ def test_adapter_calls_refuse(call, kw, code):
 
 def test_forward_and_backward_refuse_their_own():
     assert _lf(y=None) == NULL and _lf(base=P + 8) == ALIGN
-    args = (P, 1, 4, None, P, P, P, P, P, _WSB, None)
+    args = (P, 1, 4, None, P, _WSB, P, P, P, P, _WSB, None)
     assert B.lib().exl3_lora_forward(*args) == NULL
     assert _lb(dy=None) == NULL and _lb(h=None) == NULL and _lb(dx=None, g=None) == NULL
     assert _lb(dx=P + 2) == ALIGN

@@ -95,9 +95,9 @@ def _load():
     lib.exl3_lora_h_cols.restype = I
     lib.exl3_lora_workspace_bytes.argtypes = [I, I, I, I, I]
     lib.exl3_lora_workspace_bytes.restype = Z
-    lib.exl3_lora_forward.argtypes = [V, I, I, V, V, V, V, V, V, Z, V]
+    lib.exl3_lora_forward.argtypes = [V, I, I, V, V, Z, V, V, V, V, Z, V]
     lib.exl3_lora_forward.restype = I
-    lib.exl3_lora_backward.argtypes = [V, V, V, I, I, V, V, V, V, V, V, Z, V]
+    lib.exl3_lora_backward.argtypes = [V, V, V, I, I, V, V, Z, V, V, V, V, Z, V]
     lib.exl3_lora_backward.restype = I
     return lib
 
@@ -418,8 +418,8 @@ def exl3_lora_forward(x, plan, adapters: DeviceAdapters, y, workspace, base=None
     _shaped("y", y, (M, adapters.out_features), dt)
     _shaped("base", base, (M, adapters.out_features), dt)
     _shaped("h", h, (M, adapters.h_cols), dt)
-    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, adapters._ref, _ptr(plan), _ptr(base),
-                                _ptr(y), _ptr(h), _ptr(workspace), _bytes(workspace),
+    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, adapters._ref, _ptr(plan),
+                                _bytes(plan), _ptr(base), _ptr(y), _ptr(h), _ptr(workspace), _bytes(workspace),
                                 _stream(stream))
     return _check("exl3_lora_forward", rc, raise_on_error)
 
@@ -435,7 +435,7 @@ def exl3_lora_backward(dy, x, h, plan, adapters: DeviceAdapters, grads, workspac
     if grads is not None and (grads.ranks != adapters.ranks or grads.dtype != dt):
         raise ValueError("grads must hold a tensor like A and one like B for every adapter")
     rc = _lib.exl3_lora_backward(_ptr(dy), _ptr(x), _ptr(h), _DTYPE[dt], M, adapters._ref,
-                                 _ptr(plan), _ptr(dx_base), _ptr(dx),
+                                 _ptr(plan), _bytes(plan), _ptr(dx_base), _ptr(dx),
                                  None if grads is None else grads._ref, _ptr(workspace),
                                  _bytes(workspace), _stream(stream))
     return _check("exl3_lora_backward", rc, raise_on_error)

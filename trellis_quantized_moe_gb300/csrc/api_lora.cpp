@@ -25,7 +25,8 @@ int check_adapters(const exl3_adapters *ad)
 }
 
 // What forward and backward share: dtype, tables, sizes, plan, workspace.
-int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, void *ws, size_t ws_bytes)
+int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, size_t plan_bytes, void *ws,
+               size_t ws_bytes)
 {
     int rc = check_adapters(ad);
     if (rc != EXL3_OK)
@@ -38,7 +39,8 @@ int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, 
         return EXL3_E_SHAPE;
     if (!aligned(plan, 256) || !aligned(ws, 256))
         return EXL3_E_ALIGN;
-    if (ws_bytes < lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank).total)
+    if (plan_bytes < lora_plan_layout(M, ad->N).total ||
+        ws_bytes < lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank).total)
         return EXL3_E_WORKSPACE;
     return EXL3_OK;
 }
@@ -47,7 +49,7 @@ int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, 
 int product_ctas(int sms) { return sms < kLoraCtas ? sms : kLoraCtas; }
 
 // Rows up to which one launch does both products: above, the products' own
-// kernels read each weight once per 128 rows instead of once per 16.
+// kernels read each weight once per 128 rows instead of once per 8.
 constexpr int kRowsMax = 128;
 
 // h = h_scale * W1 x, y = base + y_scale * h W2 of a batch (scale_h: the
@@ -61,9 +63,10 @@ struct Products {
 };
 
 cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_adapters *ad,
-                         const exl3_adapters *grads, const void *plan, void *ws, const LoraWsLayout &L, int ctas,
+                         const exl3_adapters *grads, const void *plan, void *ws, const LoraWsLayout &L, int sms,
                          cudaStream_t stream)
 {
+    const int ctas = product_ctas(sms);
     if (M <= kRowsMax) {
         LoraRowsArgs a{};
         a.plan = static_cast<const int32_t *>(plan);
@@ -86,7 +89,7 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
         a.y = p.y;
         a.h = p.h;
         a.hdr = static_cast<int32_t *>(ws);
-        return launch_lora_rows(a, stream);
+        return launch_lora_rows(a, sms, stream);
     }
     LoraShrinkArgs sh{};
     sh.plan = static_cast<const int32_t *>(plan);
@@ -178,9 +181,9 @@ int exl3_lora_plan(const void *ids, int ids_dtype, int M, int N, void *plan, siz
 }
 
 int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *ad, const void *plan,
-                      const void *base, void *y, void *h, void *ws, size_t ws_bytes, cudaStream_t stream)
+                      size_t plan_bytes, const void *base, void *y, void *h, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    int rc = check_call(act_dtype, M, ad, plan, ws, ws_bytes);
+    int rc = check_call(act_dtype, M, ad, plan, plan_bytes, ws, ws_bytes);
     if (rc != EXL3_OK)
         return rc;
     if (M > 0 && (!x || !y))
@@ -199,16 +202,16 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
         return EXL3_OK;
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
     const Products p{x, ad->A, ad->B, ad->in_features, ad->out_features, 0, base, y, h};
-    return run_products(p, act_dtype, M, ad, nullptr, plan, ws, L, product_ctas(sms), stream) == cudaSuccess
+    return run_products(p, act_dtype, M, ad, nullptr, plan, ws, L, sms, stream) == cudaSuccess
                ? EXL3_OK
                : EXL3_E_CUDA;
 }
 
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
-                       const exl3_adapters *ad, const void *plan, const void *dx_base, void *dx,
+                       const exl3_adapters *ad, const void *plan, size_t plan_bytes, const void *dx_base, void *dx,
                        const exl3_adapters *grads, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    int rc = check_call(act_dtype, M, ad, plan, ws, ws_bytes);
+    int rc = check_call(act_dtype, M, ad, plan, plan_bytes, ws, ws_bytes);
     if (rc != EXL3_OK)
         return rc;
     if ((!dx && !grads) || (M > 0 && (!dy || (grads && (!x || !h)))))
@@ -238,7 +241,7 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
     const int ctas = product_ctas(sms);
     void *dh = static_cast<uint8_t *>(ws) + L.h;
     const Products p{dy, ad->B, ad->A, ad->out_features, ad->in_features, 1, dx_base, dx, grads ? dh : nullptr};
-    if (run_products(p, act_dtype, M, ad, grads, plan, ws, L, ctas, stream) != cudaSuccess)
+    if (run_products(p, act_dtype, M, ad, grads, plan, ws, L, sms, stream) != cudaSuccess)
         return EXL3_E_CUDA;
     if (!grads)
         return EXL3_OK;

@@ -10,7 +10,7 @@ namespace exl3 {
 
 constexpr int kLoraMagic = 0x4c6f5241;
 constexpr int kLoraTile = 128;      // rows of a prompt tile
-constexpr int kLoraSmallTile = 16;  // rows of a decode tile
+constexpr int kLoraSmallTile = 8;   // rows of a decode tile
 
 enum LoraPlanWord {
     kLpError = 0,      // sticky device error word
@@ -130,6 +130,7 @@ struct LoraExpandArgs {
 struct LoraRowsArgs {
     const int32_t *plan;
     int M, N, act_dtype, max_rank, h_cols, in_width, out_width, scale_h;
+    int ctas;                       // of one cluster (set by the launcher)
     const void *x;
     const int64_t *W1, *W2, *GA, *GB;
     const int32_t *rank;
@@ -159,12 +160,11 @@ cudaError_t lora_set_attributes();
 cudaError_t launch_lora_plan(const LoraPlanArgs &a, int ids_dtype, cudaStream_t s);
 cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
-cudaError_t launch_lora_rows(const LoraRowsArgs &a, cudaStream_t s);
+cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s);
 cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);
 cudaError_t lora_plan_set_attributes();
 cudaError_t lora_shrink_set_attributes();
 cudaError_t lora_expand_set_attributes();
 cudaError_t lora_outer_set_attributes();
-cudaError_t lora_rows_set_attributes();
 
 }  // namespace exl3

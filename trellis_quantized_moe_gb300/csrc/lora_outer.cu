@@ -422,8 +422,6 @@ cudaError_t lora_set_attributes()
         e = lora_shrink_set_attributes();
     if (e == cudaSuccess)
         e = lora_expand_set_attributes();
-    if (e == cudaSuccess)
-        e = lora_rows_set_attributes();
     return e == cudaSuccess ? lora_outer_set_attributes() : e;
 }
 

@@ -4,9 +4,9 @@
 //
 // A decode batch reads each adapter once for a row or a few, so it is bound by
 // latencies: two launches with partial sums through memory between them took
-// 10 us of GPU time for one row.  Here a cluster of eight CTAs takes a tile of
-// up to 16 rows of one adapter.  Its 64 warps share the contraction of the
-// first product in 32-wide blocks; the partial h are added warp by warp in
+// 10 us of GPU time for one row.  Here a cluster of CTAs takes a tile of up to
+// eight rows of one adapter.  Its warps share the contraction of the first
+// product in 32-wide blocks; the partial h are added warp by warp in
 // shared memory, then CTA by CTA over distributed shared memory (a fixed
 // order), so every CTA has h and goes on with its own columns of the second
 // product, whose weights and base rows are already on their way.
@@ -26,8 +26,9 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCluster = 8;
-constexpr int kWarps = kThreads / 32, kAllWarps = kCluster * kWarps;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = kLoraSmallTile;
+static_assert(kRows == 8, "a tile's rows are one MMA's N");
 
 template <bool BF>
 EXL3_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -41,9 +42,12 @@ EXL3_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
         mma_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
+EXL3_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+EXL3_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 EXL3_DEV void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 EXL3_DEV float4 ld_cluster(uint32_t addr, int rank)
@@ -64,43 +68,49 @@ EXL3_DEV uint4 ld16_or_zero(const uint8_t *p, bool in)
 }
 
 // MT: 16-rank blocks of the largest rank.  Dynamic shared memory: the warps'
-// partial h [kWarps][16 MT][16], the CTA's [16 MT][16], and h rounded [16][16 MT + 8].
+// partial h [kWarps][16 MT][8], the CTA's [16 MT][8], and h rounded [8][16 MT + 8].
 template <int MT>
 constexpr int rows_smem()
 {
-    return (kWarps + 1) * 16 * MT * 16 * 4 + 16 * (16 * MT + 8) * 2;
+    return (kWarps + 1) * 16 * MT * kRows * 4 + kRows * (16 * MT + 8) * 2;
 }
 
 template <bool BF, int MT>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT <= 4 ? 2 : 1)
-    k_lora_rows(LoraRowsArgs a)
+__global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int dtype = BF ? EXL3_BF16 : EXL3_F16;
     constexpr int kPitch = 16 * MT + 8;
     float *red = reinterpret_cast<float *>(smem);
-    float *hpart = red + kWarps * 16 * MT * 16;
-    uint16_t *h16 = reinterpret_cast<uint16_t *>(hpart + 16 * MT * 16);
+    float *hpart = red + kWarps * 16 * MT * kRows;
+    uint16_t *h16 = reinterpret_cast<uint16_t *>(hpart + 16 * MT * kRows);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int cta = blockIdx.x % kCluster, own = blockIdx.x / kCluster;
+    const int ctas = a.ctas, all_warps = ctas * kWarps;
+    const int cta = blockIdx.x % ctas, own = blockIdx.x / ctas;
     grid_dep_launch();
     auto zero_fill = [&]() {
         const size_t all = a.y ? (size_t)a.M * a.out_width / 8 : 0;
         for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < all; i += (size_t)gridDim.x * kThreads)
             static_cast<uint4 *>(a.y)[i] = make_uint4(0, 0, 0, 0);
     };
-    if (!plan_ok(a.plan, a.M, a.N)) {
+    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
+    const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.small / 4);
+    const int32_t *perm = a.plan + L.perm / 4;
+    // the tile is read along with the header that says whether it is one (the
+    // host has checked the plan's size, the launch has no more clusters than
+    // the list has room)
+    int4 t = tiles[own];
+    const bool plan_bad = !plan_ok(a.plan, a.M, a.N);
+    const int ntiles = a.plan[kLpSmallTiles], active = a.plan[kLpSmallActive];
+    if (plan_bad) {
         const bool made = a.plan[kLpMagic] == kLoraMagic && a.plan[kLpM] == a.M && a.plan[kLpN] == a.N;
         if (blockIdx.x == 0 && tid == 0)
             a.hdr[kHdrError] = made ? a.plan[kLpError] : EXL3_DERR_PLAN;
         zero_fill();
         return;
     }
-    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
-    const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.small / 4);
-    const int32_t *perm = a.plan + L.perm / 4;
-    const int ntiles = a.plan[kLpSmallTiles], active = a.plan[kLpSmallActive];
-    const int4 t = own < ntiles ? tiles[own] : make_int4(-1, 0, 0, 0);
+    if (own >= ntiles)
+        t = make_int4(-1, 0, 0, 0);
     auto entry_bad = [&](int e) {
         const int r = a.rank[e];
         bool bad = r < 0 || r > a.max_rank;
@@ -128,33 +138,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
         w2 = reinterpret_cast<const uint8_t *>(a.W2[t.x]);
     }
     const int nmt = (rank + 15) / 16;
-    const bool two = t.z > 8;                      // rows 8..15 in use
     const float alpha = rank > 0 ? a.scale[t.x] : 1.0f;
     const size_t in_pitch = (size_t)a.in_width * 2, out_pitch = (size_t)a.out_width * 2;
 
     if (nmt > 0) {
-        float acc[MT][2][4];
+        float acc[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int n = 0; n < 2; n++)
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    acc[m][n][i] = 0.0f;
-        const bool in0 = g < t.z, in1 = g + 8 < t.z;
-        const uint8_t *x0 = static_cast<const uint8_t *>(a.x) + (in0 ? perm[t.y + g] : 0) * in_pitch + q * 16;
-        const uint8_t *x1 = static_cast<const uint8_t *>(a.x) + (in1 ? perm[t.y + g + 8] : 0) * in_pitch + q * 16;
+            for (int i = 0; i < 4; i++)
+                acc[m][i] = 0.0f;
+        const bool in0 = g < t.z;
+        const uint8_t *x = static_cast<const uint8_t *>(a.x) + (in0 ? perm[t.y + g] : 0) * in_pitch + q * 16;
         const uint8_t *w = w1 + g * in_pitch + q * 16;
-        constexpr int kU = MT == 1 ? 4 : MT == 2 ? 3 : 2;      // blocks in flight
+        constexpr int kU = MT == 1 ? 6 : MT == 2 ? 4 : MT == 4 ? 2 : 1;     // blocks in flight
         const int blocks = a.in_width / 32;
-        for (int b0 = cta * kWarps + warp; b0 < blocks; b0 += kU * kAllWarps) {
-            uint4 fx0[kU], fx1[kU], fw0[kU][MT], fw1[kU][MT];
+        for (int b0 = cta * kWarps + warp; b0 < blocks; b0 += kU * all_warps) {
+            uint4 fx[kU], fw0[kU][MT], fw1[kU][MT];
 #pragma unroll
             for (int u = 0; u < kU; u++) {
-                const size_t o = (size_t)(b0 + u * kAllWarps) * 64;
-                const bool in = b0 + u * kAllWarps < blocks;
-                fx0[u] = ld16_or_zero(x0 + o, in && in0);
-                fx1[u] = ld16_or_zero(x1 + o, in && in1);
+                const size_t o = (size_t)(b0 + u * all_warps) * 64;
+                const bool in = b0 + u * all_warps < blocks;
+                fx[u] = ld16_or_zero(x + o, in && in0);
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
                     fw0[u][m] = ld16_or_zero(w + o + m * 16 * in_pitch, in && 16 * m + g < rank);
@@ -167,31 +172,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
                 for (int m = 0; m < MT; m++)
                     if (m < nmt) {
                         const uint4 p = fw0[u][m], r = fw1[u][m];
-                        mma16816<BF>(acc[m][0], p.x, r.x, p.y, r.y, fx0[u].x, fx0[u].y);
-                        mma16816<BF>(acc[m][0], p.z, r.z, p.w, r.w, fx0[u].z, fx0[u].w);
-                        if (two) {
-                            mma16816<BF>(acc[m][1], p.x, r.x, p.y, r.y, fx1[u].x, fx1[u].y);
-                            mma16816<BF>(acc[m][1], p.z, r.z, p.w, r.w, fx1[u].z, fx1[u].w);
-                        }
+                        mma16816<BF>(acc[m], p.x, r.x, p.y, r.y, fx[u].x, fx[u].y);
+                        mma16816<BF>(acc[m], p.z, r.z, p.w, r.w, fx[u].z, fx[u].w);
                     }
         }
-        float *mine = red + warp * (16 * MT * 16);
+        float *mine = red + warp * (16 * MT * kRows);
 #pragma unroll
         for (int m = 0; m < MT; m++)
-            if (m < nmt)
-#pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    *reinterpret_cast<float2 *>(mine + (16 * m + g) * 16 + 8 * n + 2 * q) =
-                        make_float2(acc[m][n][0], acc[m][n][1]);
-                    *reinterpret_cast<float2 *>(mine + (16 * m + g + 8) * 16 + 8 * n + 2 * q) =
-                        make_float2(acc[m][n][2], acc[m][n][3]);
-                }
+            if (m < nmt) {
+                *reinterpret_cast<float2 *>(mine + (16 * m + g) * kRows + 2 * q) = make_float2(acc[m][0], acc[m][1]);
+                *reinterpret_cast<float2 *>(mine + (16 * m + g + 8) * kRows + 2 * q) =
+                    make_float2(acc[m][2], acc[m][3]);
+            }
     }
     // the second product's first weights and base rows, on their way during the reduction
     constexpr int kPre = MT < 4 ? MT : 4;
     // (rows that only keep base need nothing when it is y already)
     const int groups = a.y && own < ntiles && (nmt > 0 || a.base != a.y) ? a.out_width / 64 : 0;
-    const int first = warp * kCluster + cta;
+    const int first = warp * ctas + cta;
     // W2 rows of 16-rank step s at column group `grp`
     auto load_w2 = [&](int s, int grp, uint4 (&f)[4]) {
         const uint8_t *p = w2 + (size_t)grp * 128 + g * 16;
@@ -201,20 +199,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
             f[i] = ld16_or_zero(p + j * out_pitch, j < rank);
         }
     };
-    int yrow[4];                                   // rows 2q, 2q+1, 2q+8, 2q+9 of the tile
+    int yrow[2];                                   // rows 2q, 2q+1 of the tile
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = 2 * q + (i & 1) + (i >> 1) * 8;
-        yrow[i] = r < t.z ? perm[t.y + r] : -1;
-    }
-    auto load_base = [&](int grp, uint4 (&f)[4]) {
+    for (int i = 0; i < 2; i++)
+        yrow[i] = 2 * q + i < t.z ? perm[t.y + 2 * q + i] : -1;
+    auto load_base = [&](int grp, uint4 (&f)[2]) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 2; i++)
             f[i] = ld16_or_zero(static_cast<const uint8_t *>(a.base) + (yrow[i] < 0 ? 0 : yrow[i]) * out_pitch +
                                     (size_t)grp * 128 + g * 16,
                                 a.base != nullptr && yrow[i] >= 0);
     };
-    uint4 pre[kPre][4], fb[4];
+    uint4 pre[kPre][4], fb[2];
     if (first < groups) {
 #pragma unroll
         for (int s = 0; s < kPre; s++)
@@ -232,12 +228,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
         a.hdr[kHdrError] = 0;
     if (own >= ntiles)
         return;                                    // the whole cluster
-    const int n4 = nmt * 16 * 4;                   // float4s of h, [rank][row]
+    const int n4 = nmt * 16 * (kRows / 4);         // float4s of h, [rank][row]
     for (int i = tid; i < n4; i += kThreads) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; w++) {
-            const float4 f = reinterpret_cast<const float4 *>(red + w * (16 * MT * 16))[i];
+            const float4 f = reinterpret_cast<const float4 *>(red + w * (16 * MT * kRows))[i];
             v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
         }
         reinterpret_cast<float4 *>(hpart)[i] = v;
@@ -245,13 +241,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
     cluster_sync();
     const float hs = a.scale_h ? alpha : 1.0f;
     for (int i = tid; i < n4; i += kThreads) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), f[8];
 #pragma unroll
-        for (int r = 0; r < kCluster; r++) {
-            const float4 f = ld_cluster(smem_addr(hpart) + i * 16, r);
-            v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
-        }
-        const int j = i >> 2, r = (i & 3) * 4;
+        for (int r = 0; r < 8; r++)
+            f[r] = ld_cluster(smem_addr(hpart) + i * 16, min(r, ctas - 1));
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+            if (r < ctas) {
+                v.x += f[r].x; v.y += f[r].y; v.z += f[r].z; v.w += f[r].w;
+            }
+        const int j = i / (kRows / 4), r = i % (kRows / 4) * 4;
         const float z[4] = {v.x * hs, v.y * hs, v.z * hs, v.w * hs};
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -261,17 +260,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
                 static_cast<uint16_t *>(a.h)[(size_t)(t.y + r + e) * a.h_cols + j] = u;
         }
     }
+    // from here on the cluster's other CTAs may still be reading hpart
+    cluster_arrive();
     __syncthreads();
     const float ys = a.scale_h ? 1.0f : alpha;
-    for (int grp = first; grp < groups; grp += kAllWarps) {
-        float acc[4][2][4];
+    for (int grp = first; grp < groups; grp += all_warps) {
+        float acc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int n = 0; n < 2; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    acc[i][n][e] = 0.0f;
+            for (int e = 0; e < 4; e++)
+                acc[i][e] = 0.0f;
         if (grp != first)
             load_base(grp, fb);
 #pragma unroll
@@ -286,7 +285,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
                     load_w2(s, grp, f);
                 }
                 const uint32_t *hb = reinterpret_cast<const uint32_t *>(h16 + g * kPitch + 16 * s + 2 * q);
-                const uint32_t b0 = hb[0], b1 = hb[4], c0 = hb[8 * kPitch / 2], c1 = hb[8 * kPitch / 2 + 4];
+                const uint32_t b0 = hb[0], b1 = hb[4];
                 const uint32_t *pa = reinterpret_cast<const uint32_t *>(&f[0]);
                 const uint32_t *pb = reinterpret_cast<const uint32_t *>(&f[1]);
                 const uint32_t *pc = reinterpret_cast<const uint32_t *>(&f[2]);
@@ -296,38 +295,45 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, MT 
                     const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
                     const uint32_t a0 = prmt(pa[i / 2], pb[i / 2], sel), a1 = prmt(pa[2 + i / 2], pb[2 + i / 2], sel);
                     const uint32_t a2 = prmt(pc[i / 2], pd[i / 2], sel), a3 = prmt(pc[2 + i / 2], pd[2 + i / 2], sel);
-                    mma16816<BF>(acc[i][0], a0, a1, a2, a3, b0, b1);
-                    if (two)
-                        mma16816<BF>(acc[i][1], a0, a1, a2, a3, c0, c1);
+                    mma16816<BF>(acc[i], a0, a1, a2, a3, b0, b1);
                 }
             }
-        // lane: rows 2q, 2q+1 (accumulators 0, 1 of columns 0-3; 2, 3 of columns 4-7), then 8 more
+        // lane: rows 2q, 2q+1 (accumulators 0, 1 of columns 0-3; 2, 3 of columns 4-7)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < 2; i++) {
             if (yrow[i] < 0)
                 continue;
-            const int n = i >> 1, odd = i & 1;
             uint4 u = fb[i];
             if (nmt > 0) {
                 uint32_t *pu = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const float2 f = unpack2(pu[e], dtype);
-                    const int lo = (2 * e) & 3, up = (e >= 2) * 2 + odd;
-                    pu[e] = pack2(fmaf(ys, acc[lo][n][up], f.x), fmaf(ys, acc[lo + 1][n][up], f.y), dtype);
+                    const int lo = (2 * e) & 3, up = (e >= 2) * 2 + i;
+                    pu[e] = pack2(fmaf(ys, acc[lo][up], f.x), fmaf(ys, acc[lo + 1][up], f.y), dtype);
                 }
             }
             *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.y) + yrow[i] * out_pitch + (size_t)grp * 128 + g * 16) = u;
         }
     }
-    cluster_sync();                                // nobody reads this CTA's partials any more
+    cluster_wait();                                // nobody reads this CTA's partials any more
 }
 
 template <bool BF, int MT>
 cudaError_t launch(const LoraRowsArgs &a, int clusters, cudaStream_t s)
 {
-    k_lora_rows<BF, MT><<<clusters * kCluster, kThreads, rows_smem<MT>(), s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = a.ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(clusters * a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = rows_smem<MT>();
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_lora_rows<BF, MT>, a);
 }
 
 template <bool BF>
@@ -344,19 +350,13 @@ cudaError_t launch_ranks(const LoraRowsArgs &a, int clusters, cudaStream_t s)
 
 }  // namespace lora
 
-cudaError_t lora_rows_set_attributes()
-{
-    cudaError_t e = cudaFuncSetAttribute(lora::k_lora_rows<true, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         lora::rows_smem<8>());
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(lora::k_lora_rows<false, 8>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, lora::rows_smem<8>());
-}
-
-cudaError_t launch_lora_rows(const LoraRowsArgs &a, cudaStream_t s)
+cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s)
 {
     // at most this many tiles: full ones, and one more per adapter in use and for rows without one
     const int clusters = a.M / kLoraSmallTile + (a.N < a.M ? a.N : a.M) + 1;
+    // as many CTAs per tile as fit in one wave (two per SM), two at least: a
+    // second wave starts with the whole chain of look-ups again
+    a.ctas = clusters * 8 <= 2 * sms ? 8 : clusters * 4 <= 2 * sms ? 4 : 2;
     return a.act_dtype == EXL3_BF16 ? lora::launch_ranks<true>(a, clusters, s)
                                     : lora::launch_ranks<false>(a, clusters, s);
 }
