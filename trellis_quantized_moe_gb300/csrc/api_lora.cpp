@@ -48,9 +48,14 @@ int check_call(int act_dtype, int M, const exl3_adapters *ad, const void *plan, 
 // One CTA per SM shares a product's work; the workspace knows kLoraCtas of them.
 int product_ctas(int sms) { return sms < kLoraCtas ? sms : kLoraCtas; }
 
-// Rows up to which one launch does both products: above, the products' own
-// kernels read each weight once per 128 rows instead of once per 8.
-constexpr int kRowsMax = 128;
+// Rows up to which one launch does both products.  It reads a weight once per
+// eight rows (from L2), the products' own kernels once per 128, at the price of
+// two launches and partial sums between them.  GPU time of a call, one launch /
+// two (bf16, us): 5120 -> 1536, rank 16: 1 row 4.6 / 10.6, 512 rows 6.6 / 15.0,
+// 1024 rows 8.7 / 15.6, 1500 rows 14.1 / 16.4, 2048 rows 16.1 / 17.3, 4096 rows
+// 31.5 / 20.3; rank 64: 1024 rows 17.7 / 19.9, 1500 rows 28.4 / 20.8; 1536 ->
+// 5120: rank 16, 1024 rows 11.3 / 15.6, 1500 rows 20.1 / 15.9.
+constexpr int kRowsMax = 1024;
 
 // h = h_scale * W1 x, y = base + y_scale * h W2 of a batch (scale_h: the
 // adapter's scale goes to h instead of y), and the check of the tables.
