@@ -113,8 +113,25 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
     sh.GA = grads ? grads->A : nullptr;
     sh.GB = grads ? grads->B : nullptr;
     sh.hdr = static_cast<int32_t *>(ws);
-    const cudaError_t e = launch_lora_shrink(sh, ctas, stream);
+    cudaError_t e = launch_lora_shrink(sh, ctas, stream);
     if (e != cudaSuccess)
+        return e;
+    LoraJoinArgs jn{};
+    jn.plan = sh.plan;
+    jn.M = M;
+    jn.N = sh.N;
+    jn.act_dtype = act_dtype;
+    jn.h_cols = sh.h_cols;
+    jn.scale_h = p.scale_h;
+    jn.part = sh.part;
+    jn.shrink_width = sh.width;
+    jn.shrink_ctas = ctas;
+    jn.rank = ad->rank;
+    jn.scale = ad->scale;
+    jn.h = p.h;
+    jn.hdr = sh.hdr;
+    e = launch_lora_join(jn, stream);
+    if (e != cudaSuccess || !p.y)
         return e;
     LoraExpandArgs ex{};
     ex.plan = sh.plan;
@@ -124,9 +141,6 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
     ex.h_cols = sh.h_cols;
     ex.width = p.out_width;
     ex.scale_h = p.scale_h;
-    ex.part = sh.part;
-    ex.shrink_width = sh.width;
-    ex.shrink_ctas = ctas;
     ex.h = p.h;
     ex.W = p.W2;
     ex.rank = ad->rank;
@@ -206,7 +220,8 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
     if (M == 0)
         return EXL3_OK;
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
-    const Products p{x, ad->A, ad->B, ad->in_features, ad->out_features, 0, base, y, h};
+    const Products p{x, ad->A, ad->B, ad->in_features, ad->out_features, 0, base, y,
+                     h ? h : static_cast<uint8_t *>(ws) + L.h};
     return run_products(p, act_dtype, M, ad, nullptr, plan, ws, L, sms, stream) == cudaSuccess
                ? EXL3_OK
                : EXL3_E_CUDA;
@@ -245,7 +260,7 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
     const int ctas = product_ctas(sms);
     void *dh = static_cast<uint8_t *>(ws) + L.h;
-    const Products p{dy, ad->B, ad->A, ad->out_features, ad->in_features, 1, dx_base, dx, grads ? dh : nullptr};
+    const Products p{dy, ad->B, ad->A, ad->out_features, ad->in_features, 1, dx_base, dx, dh};
     if (run_products(p, act_dtype, M, ad, grads, plan, ws, L, sms, stream) != cudaSuccess)
         return EXL3_E_CUDA;
     if (!grads)

@@ -106,17 +106,26 @@ struct LoraShrinkArgs {
     int32_t *hdr;
 };
 
-// expand: h = h_scale * (sum of shrink's partials), rounded to the activation
-// type (and kept in `h` where asked), then
-//   y[perm[s]][n] = base[perm[s]][n] + y_scale * sum_j h[s][j] W_a[j][n].
-// h_scale / y_scale: the adapter's scale where `scale_h` / not, else 1.
-// y == nullptr: only h.
+// join: h[s][j] = h_scale * (sum of shrink's partials), rounded to the activation
+// type, zero from the adapter's rank up to the next multiple of 16; h_scale:
+// the adapter's scale where `scale_h`, else 1.
+struct LoraJoinArgs {
+    const int32_t *plan;
+    int M, N, act_dtype, h_cols, scale_h;
+    const float *part;
+    int shrink_width, shrink_ctas;  // the shares that cut shrink's tiles
+    const int32_t *rank;
+    const float *scale;
+    void *h;
+    const int32_t *hdr;
+};
+
+// expand: y[perm[s]][n] = base[perm[s]][n] + y_scale * sum_j h[s][j] W_a[j][n];
+// y_scale: 1 where `scale_h`, else the adapter's scale.
 struct LoraExpandArgs {
     const int32_t *plan;
     int M, N, act_dtype, h_cols, width, scale_h;
-    const float *part;
-    int shrink_width, shrink_ctas;  // the shares that cut shrink's tiles
-    void *h;
+    const void *h;
     const int64_t *W;
     const int32_t *rank;
     const float *scale;
@@ -159,6 +168,7 @@ struct LoraOuterArgs {
 cudaError_t lora_set_attributes();
 cudaError_t launch_lora_plan(const LoraPlanArgs &a, int ids_dtype, cudaStream_t s);
 cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s);
+cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s);
 cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);

@@ -4,7 +4,7 @@
 //
 // Bound by reading base and writing y once (2 r products per 4 bytes).  An
 // item is a tile of 128 rows x NW outputs; a CTA takes a contiguous share of
-// the items, so a tile's h is joined once per CTA and stays in shared memory
+// the items, so a tile's h is fetched once per CTA and stays in shared memory
 // for its output blocks.  Two groups of loader warps take turns on the items
 // and copy base rows (gathered) and the W block by cp.async; an epilogue
 // thread owns a row, adds its accumulator (TMEM) to the row in place, and the
@@ -20,9 +20,8 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 640;       // 8 loader, 8 epilogue warps, MMA warp, 3 join warps
-constexpr int kMmaWarp = 16, kJoinWarp = 17;
-constexpr int kFirstJoin = 352;     // threads that join a CTA's first tile: epilogue and join warps
+constexpr int kThreads = 640;       // 8 loader, 8 epilogue warps, MMA warp, 3 warps for h
+constexpr int kMmaWarp = 16, kHWarp = 17, kHThreads = 96;
 constexpr int kTBufs = 4;           // TMEM accumulators
 constexpr int kMaxRing = 4;
 
@@ -47,70 +46,10 @@ EXL3_HD inline Geom geom(int h_cols)
 EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
 
 struct Ctl {
-    uint64_t hfirst, hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
+    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
     uint32_t tmem;
     int abort;
 };
-
-// Joins h of one tile, thread jt of n (a multiple of 32): the partials of CTAs
-// c0..c1 in that order, scaled, zero from the rank on, rounded; into shared
-// memory (hs) and, with keep, into a.h.  A thread has four columns of up to
-// eight rows of two partials in flight: they lie in L2, and one load at a time
-// took longer (r = 128: 40 us a tile) than everything else in the kernel.
-EXL3_DEV void join_h(const LoraExpandArgs &a, const int4 &t, int rank, int c0, int c1, float alpha, uint8_t *hs,
-                     bool keep, int jt, int n)
-{
-    constexpr int kU = 8;
-    const int rp = (rank + 15) / 16 * 16;
-    const int lq = rp <= 16 ? 2 : rp <= 32 ? 3 : rp <= 64 ? 4 : 5;   // lanes per row: 2^lq
-    const int j = (jt & ((1 << lq) - 1)) * 4, step = n >> lq;
-    if (j >= rp)
-        return;
-    const size_t cta = 128 * (size_t)a.h_cols;
-    for (int r0 = jt >> lq; r0 < t.z; r0 += kU * step) {
-        float4 v[kU], f[kU];
-#pragma unroll
-        for (int u = 0; u < kU; u++)
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float *p = a.part + (size_t)(t.y + r0) * a.h_cols + j + c0 * cta;
-        if (t.z <= step) {                         // one row a thread: eight partials in flight
-            for (int c = c0; c <= c1; c += kU, p += kU * cta) {
-#pragma unroll
-                for (int u = 0; u < kU; u++)
-                    f[u] = *reinterpret_cast<const float4 *>(p + min(u, c1 - c) * cta);
-#pragma unroll
-                for (int u = 0; u < kU; u++)
-                    if (c + u <= c1) {
-                        v[0].x += f[u].x; v[0].y += f[u].y; v[0].z += f[u].z; v[0].w += f[u].w;
-                    }
-            }
-        } else {
-            for (int c = c0; c <= c1; c++, p += cta) {
-#pragma unroll
-                for (int u = 0; u < kU; u++)
-                    f[u] = *reinterpret_cast<const float4 *>(p + (size_t)min(u * step, t.z - 1 - r0) * a.h_cols);
-#pragma unroll
-                for (int u = 0; u < kU; u++) {
-                    v[u].x += f[u].x; v[u].y += f[u].y; v[u].z += f[u].z; v[u].w += f[u].w;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kU; u++) {
-            const int r = r0 + u * step;
-            if (r >= t.z)
-                break;
-            const float4 w = v[u];
-            const uint2 o = make_uint2(
-                pack2(j < rank ? w.x * alpha : 0.f, j + 1 < rank ? w.y * alpha : 0.f, a.act_dtype),
-                pack2(j + 2 < rank ? w.z * alpha : 0.f, j + 3 < rank ? w.w * alpha : 0.f, a.act_dtype));
-            if (hs)
-                *reinterpret_cast<uint2 *>(hs + (j >> 6) * (128 * 128) + swz(r, (j & 63) >> 3) + (j & 4) * 2) = o;
-            if (keep)
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = o;
-        }
-    }
-}
 
 template <int NW>
 __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
@@ -121,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     grid_dep_launch();
     // an error zero-fills y: 128 threads of every CTA, this one the i0-th
     auto zero_fill = [&](int i0) {
-        const size_t all = a.y && i0 < 128 ? (size_t)a.M * a.width / 8 : 0;
+        const size_t all = i0 < 128 ? (size_t)a.M * a.width / 8 : 0;
         for (size_t i = (size_t)blockIdx.x * 128 + i0; i < all; i += (size_t)gridDim.x * 128)
             static_cast<uint4 *>(a.y)[i] = make_uint4(0, 0, 0, 0);
     };
@@ -133,11 +72,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     const int4 *tiles = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4);
     const int32_t *perm = a.plan + L.perm / 4;
     const int active = a.plan[kLpActive];
-    const int sks = a.shrink_width / kShrinkK;
-    const int sper = lora_share(active * sks, a.shrink_ctas, kShrinkMin);
     // rows without an adapter need nothing when y is base already
-    const int ntiles = !a.y || a.base == a.y ? active : a.plan[kLpTiles];
-    const int nb = a.y ? a.width / NW : 1;
+    const int ntiles = a.base == a.y ? active : a.plan[kLpTiles];
+    const int nb = a.width / NW;
     const int total = ntiles * nb, per = lora_share(total, gridDim.x, 1);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
     if (begin >= end) {
@@ -150,9 +87,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     uint8_t *hbuf = smem, *ring = smem + 2 * g.h_bytes;
     volatile int *abort = &c.abort;
     if (tid == 0) {
-        mbar_init(&c.hfirst, kFirstJoin);
         for (int i = 0; i < 2; i++) {
-            mbar_init(&c.hfull[i], 96);
+            mbar_init(&c.hfull[i], kHThreads);
             mbar_init(&c.hempty[i], 1);
         }
         for (int i = 0; i < kMaxRing; i++) {
@@ -182,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         return r < 0 || r > a.h_cols || !w || (w & 15) ? 0 : r;
     };
 
-    if (warp < 8 && a.y) {
+    if (warp < 8) {
         // group 0 takes the even items of the share, group 1 the odd ones
         constexpr int kLanes = NW / 8, kStep = 128 / kLanes, kN = 128 / kStep;   // lanes per row, rows a pass
         const int group = warp >> 2, gt = tid & 127, ch = gt % kLanes, r0 = gt / kLanes;
@@ -238,51 +174,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             put.next2(g.nslots);
         }
         cp_async_wait_all();
-    } else if (warp >= kJoinWarp) {
-        grid_dep_wait();                           // the partials and the error word
-        const bool bad = a.hdr[kHdrError] != 0;
+    } else if (warp >= kHWarp) {
+        // h of each tile, K-major: rp / 8 chunks a row
+        const int ht = tid - kHWarp * 32;
         Ring hb;
+        grid_dep_wait();                           // h comes from the kernel before
         for (int s = begin; s < end;) {
-            const int tile = s / nb, last = min(end, (tile + 1) * nb);
+            const int tile = s / nb;
             const int4 t = tiles[tile];
-            const int rank = tile_rank(t);
+            const int rank = tile_rank(t), hc = (rank + 15) / 16 * 2;
             if (rank > 0) {
-                const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
-                const int c0 = tile * sks / sper, c1 = ((tile + 1) * sks - 1) / sper;
-                const bool first = a.y && s == begin;
-                if (a.y && !wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
+                if (!wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
                     break;
-                if (!bad)
-                    join_h(a, t, rank, c0, c1, alpha, a.y ? hbuf + hb.slot * g.h_bytes : nullptr,
-                           a.h != nullptr && s % nb == 0, tid - kJoinWarp * 32, first ? kFirstJoin : 96);
-                if (a.y) {
-                    fence_proxy();
-                    mbar_arrive(first ? &c.hfirst : &c.hfull[hb.slot]);
-                    hb.next(2);
+                const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
+                const uint8_t *h = static_cast<const uint8_t *>(a.h) + (size_t)t.y * a.h_cols * 2;
+                for (int i = ht; i < t.z * hc; i += kHThreads) {
+                    const int r = i / hc, q = i % hc;
+                    cp_async16(hs + (q >> 3) * (128 * 128) + swz(r, q & 7), h + (size_t)r * a.h_cols * 2 + q * 16, true);
                 }
+                cp_async_arrive(&c.hfull[hb.slot]);
+                hb.next(2);
             }
-            s = last;
+            s = (tile + 1) * nb;
         }
-    } else if (warp >= 8 && warp < kMmaWarp && a.y) {
+        cp_async_wait_all();
+    } else if (warp >= 8 && warp < kMmaWarp) {
         // warps 8 + q and 12 + q: rows 32 q .. 32 q + 31, half the columns each
         constexpr int kCols = NW / 2, kLanes = kCols / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
         const int q = warp & 3, c0 = (warp - 8) / 4 * kCols, row = 32 * q + lane;
-        grid_dep_wait();                           // the error word and the partials
+        grid_dep_wait();                           // the error word
         const bool bad = a.hdr[kHdrError] != 0;
         Ring t4, in;
         for (int s = begin; s < end;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
             const int4 t = tiles[tile];
-            const int rank = tile_rank(t);
-            const bool mma = rank > 0;
-            if (mma && s == begin) {
-                // nothing to do before the first tile's h is there: help joining it
-                if (!bad)
-                    join_h(a, t, rank, tile * sks / sper, ((tile + 1) * sks - 1) / sper,
-                           a.scale_h ? a.scale[t.x] : 1.0f, hbuf, a.h != nullptr && s % nb == 0, tid - 160, kFirstJoin);
-                fence_proxy();
-                mbar_arrive(&c.hfirst);
-            }
+            const bool mma = tile_rank(t) > 0;
             const float alpha = mma && !a.scale_h ? a.scale[t.x] : 1.0f;
             const size_t off = row < t.z ? (size_t)perm[t.y + row] * a.width * 2 : 0;
             const int rows = bad ? 0 : min(32, t.z - 32 * q);      // of this warp, to be written
@@ -344,9 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         }
         if (bad)
             zero_fill(tid - 256);
-    } else if (warp == kMmaWarp && lane == 0 && a.y) {
+    } else if (warp == kMmaWarp && lane == 0) {
         Ring hb, in, t4;
-        uint32_t hphase[2] = {0, 0};               // the first tile takes a slot without its hfull
         bool ok = true;
         for (int s = begin; s < end && ok;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
@@ -357,11 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 continue;
             }
             const uint32_t id = idesc(NW, a.act_dtype, 0, 1);
-            const bool first = s == begin;
-            if (!(ok = wait_bar(first ? &c.hfirst : &c.hfull[hb.slot], first ? 0 : hphase[hb.slot], abort, a.hdr)))
+            if (!(ok = wait_bar(&c.hfull[hb.slot], hb.phase, abort, a.hdr)))
                 break;
-            if (!first)
-                hphase[hb.slot] ^= 1;
             const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
             for (; s < last; s++) {
                 if (!(ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr) &&

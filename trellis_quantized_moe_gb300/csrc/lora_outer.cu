@@ -26,7 +26,7 @@ constexpr int kHalfCols = 128;                   // TMEM columns of one 128-colu
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 6;
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 4;       // blocks per cut item
+constexpr int kJoinParts = 8;       // blocks per cut item
 constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
 
 EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * kBlock; }
@@ -326,10 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         tmem_free(c.tmem, 4 * kHalfCols);
 }
 
-// Blocks 4c .. 4c + 3, c < ctas: a quarter each of the item that the boundary
+// Blocks 8c .. 8c + 7, c < ctas: an eighth each of the item that the boundary
 // between shares c and c + 1 cuts, if c holds the item's first stage.  The
 // other blocks zero the gradients of adapters without rows.
-__global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
+__global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs a)
 {
     if (!plan_ok(a.plan, a.M, a.N))
         return;
@@ -368,17 +368,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraOuterArgs a)
         return;
     uint8_t *out = reinterpret_cast<uint8_t *>(a.p[it.p].G[it.e]);
     // four columns a thread
-    constexpr int kU = 4, kStep = kJoinParts * kJoinThreads;
+    constexpr int kU = 4, kStep = kJoinParts * kJoinThreads, kC = 2;   // kU * kC loads in flight
     for (int i0 = (blockIdx.x % kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * quads; i0 += kU * kStep) {
         float4 v[kU] = {};
-        for (int c = c0; c <= c1; c++) {
-            const float *p = a.part + (2 * (size_t)c + (max(it.first, c * per) > c * per)) * slot;
+        for (int c = c0; c <= c1; c += kC) {
+            float4 f[kC][kU];
 #pragma unroll
-            for (int u = 0; u < kU; u++)
-                if (i0 + u * kStep < rank * quads) {
+            for (int d = 0; d < kC; d++) {
+                const float *p = a.part + (2 * (size_t)(c + d) + (max(it.first, (c + d) * per) > (c + d) * per)) * slot;
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
                     const int i = i0 + u * kStep;
-                    const float4 f = *reinterpret_cast<const float4 *>(p + i / quads * kOuterN + i % quads * 4);
-                    v[u].x += f.x; v[u].y += f.y; v[u].z += f.z; v[u].w += f.w;
+                    f[d][u] = c + d <= c1 && i < rank * quads
+                                  ? *reinterpret_cast<const float4 *>(p + i / quads * kOuterN + i % quads * 4)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kC; d++)
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
+                    v[u].x += f[d][u].x; v[u].y += f[d][u].y; v[u].z += f[d][u].z; v[u].w += f[d][u].w;
                 }
         }
 #pragma unroll
@@ -411,7 +421,7 @@ cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s)
         if (e != cudaSuccess)
             return e;
     }
-    return lora::launch_dependent(lora::k_lora_join, a.ctas * lora::kJoinParts + lora::kZeroBlocks,
+    return lora::launch_dependent(lora::k_lora_outer_join, a.ctas * lora::kJoinParts + lora::kZeroBlocks,
                                   lora::kJoinThreads, 0, s, a);
 }
 

@@ -6,7 +6,7 @@
 // The tiles' contractions, laid end to end as 128-wide stages, are shared out
 // evenly over one CTA per SM whatever the tile count (a batch of few rows is
 // split over its width, one of many is not); a tile cut by the shares leaves
-// one fp32 partial per CTA, which the expand kernel adds in CTA order.  A stage
+// one fp32 partial per CTA, which k_lora_join adds in CTA order.  A stage
 // is 128 rows x 256 bytes of x and the adapter's rank x 256 bytes of W, copied
 // by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring by two
 // groups of loader warps that take turns; one thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
@@ -259,9 +259,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         tmem_free(c.tmem, 2 * kBufCols);
 }
 
+// Adds a tile's partials and rounds them once to the second product's operand.
+// Four blocks per tile, 32 rows each; a thread has four columns of a row and
+// the partials of four CTAs in flight (they lie in L2).
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+
+__global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
+{
+    grid_dep_launch();
+    if (!plan_ok(a.plan, a.M, a.N))
+        return;
+    const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
+    const int active = a.plan[kLpActive], tile = blockIdx.x / (kLoraTile / kJoinRows);
+    if (tile >= active)
+        return;
+    const int4 t = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4)[tile];
+    const int first = blockIdx.x % (kLoraTile / kJoinRows) * kJoinRows;
+    const int rank = min(max(a.rank[t.x], 0), a.h_cols), rp = (rank + 15) / 16 * 16;
+    const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
+    const int ks = a.shrink_width / kShrinkK, per = lora_share(active * ks, a.shrink_ctas, kShrinkMin);
+    const int c0 = tile * ks / per, c1 = ((tile + 1) * ks - 1) / per;
+    const int lq = rp <= 16 ? 2 : rp <= 32 ? 3 : rp <= 64 ? 4 : 5;       // lanes per row: 2^lq
+    const int j = (threadIdx.x & ((1 << lq) - 1)) * 4;
+    grid_dep_wait();
+    if (j >= rp || a.hdr[kHdrError])
+        return;
+    const size_t cta = 128 * (size_t)a.h_cols;
+    for (int r = first + (threadIdx.x >> lq); r < min(t.z, first + kJoinRows); r += kJoinThreads >> lq) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *p = a.part + (size_t)(t.y + r) * a.h_cols + j + c0 * cta;
+        constexpr int kC = 4;
+        for (int c = c0; c <= c1; c += kC, p += kC * cta) {
+            float4 f[kC];
+#pragma unroll
+            for (int d = 0; d < kC; d++)
+                f[d] = *reinterpret_cast<const float4 *>(p + min(d, c1 - c) * cta);
+#pragma unroll
+            for (int d = 0; d < kC; d++)
+                if (c + d <= c1) {
+                    v.x += f[d].x; v.y += f[d].y; v.z += f[d].z; v.w += f[d].w;
+                }
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = make_uint2(
+            pack2(j < rank ? v.x * alpha : 0.f, j + 1 < rank ? v.y * alpha : 0.f, a.act_dtype),
+            pack2(j + 2 < rank ? v.z * alpha : 0.f, j + 3 < rank ? v.w * alpha : 0.f, a.act_dtype));
+    }
+}
+
 }  // namespace
 
 }  // namespace lora
+
+cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s)
+{
+    const int tiles = a.M / kLoraTile + (a.N < a.M ? a.N : a.M);       // of adapters, at most
+    return lora::launch_dependent(lora::k_lora_join, tiles * (kLoraTile / lora::kJoinRows), lora::kJoinThreads, 0, s,
+                                  a);
+}
 
 cudaError_t lora_shrink_set_attributes()
 {
