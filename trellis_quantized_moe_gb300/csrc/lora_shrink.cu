@@ -260,9 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
 }
 
 // Adds a tile's partials and rounds them once to the second product's operand.
-// Four blocks per tile, 32 rows each; a thread has four columns of a row and
-// the partials of four CTAs in flight (they lie in L2).
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+// A thread has four columns of one row and the partials of four CTAs in flight
+// (they lie in L2); a block takes as many rows as its threads have at the
+// largest rank.
+constexpr int kJoinThreads = 256;
+
+EXL3_HD inline int join_lanes(int rank_cols) { return rank_cols <= 16 ? 4 : rank_cols <= 32 ? 8 : rank_cols <= 64 ? 16 : 32; }
+EXL3_HD inline int join_rows(int h_cols) { return kJoinThreads / join_lanes(h_cols); }
 
 __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
 {
@@ -270,22 +274,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
     if (!plan_ok(a.plan, a.M, a.N))
         return;
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
-    const int active = a.plan[kLpActive], tile = blockIdx.x / (kLoraTile / kJoinRows);
+    const int rows = join_rows(a.h_cols), blocks = kLoraTile / rows;
+    const int active = a.plan[kLpActive], tile = blockIdx.x / blocks;
     if (tile >= active)
         return;
     const int4 t = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4)[tile];
-    const int first = blockIdx.x % (kLoraTile / kJoinRows) * kJoinRows;
     const int rank = min(max(a.rank[t.x], 0), a.h_cols), rp = (rank + 15) / 16 * 16;
     const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
     const int ks = a.shrink_width / kShrinkK, per = lora_share(active * ks, a.shrink_ctas, kShrinkMin);
     const int c0 = tile * ks / per, c1 = ((tile + 1) * ks - 1) / per;
-    const int lq = rp <= 16 ? 2 : rp <= 32 ? 3 : rp <= 64 ? 4 : 5;       // lanes per row: 2^lq
-    const int j = (threadIdx.x & ((1 << lq) - 1)) * 4;
+    const int lanes = join_lanes(a.h_cols), j = threadIdx.x % lanes * 4;
+    const int r = blockIdx.x % blocks * rows + threadIdx.x / lanes;
     grid_dep_wait();
-    if (j >= rp || a.hdr[kHdrError])
-        return;
-    const size_t cta = 128 * (size_t)a.h_cols;
-    for (int r = first + (threadIdx.x >> lq); r < min(t.z, first + kJoinRows); r += kJoinThreads >> lq) {
+    const int err = a.hdr[kHdrError];              // looked at before the store only
+    if (j < rp && r < t.z) {
+        const size_t cta = 128 * (size_t)a.h_cols;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         const float *p = a.part + (size_t)(t.y + r) * a.h_cols + j + c0 * cta;
         constexpr int kC = 4;
@@ -300,9 +303,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
                     v.x += f[d].x; v.y += f[d].y; v.z += f[d].z; v.w += f[d].w;
                 }
         }
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = make_uint2(
-            pack2(j < rank ? v.x * alpha : 0.f, j + 1 < rank ? v.y * alpha : 0.f, a.act_dtype),
-            pack2(j + 2 < rank ? v.z * alpha : 0.f, j + 3 < rank ? v.w * alpha : 0.f, a.act_dtype));
+        if (err == 0)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = make_uint2(
+                pack2(j < rank ? v.x * alpha : 0.f, j + 1 < rank ? v.y * alpha : 0.f, a.act_dtype),
+                pack2(j + 2 < rank ? v.z * alpha : 0.f, j + 3 < rank ? v.w * alpha : 0.f, a.act_dtype));
     }
 }
 
@@ -313,8 +317,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
 cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s)
 {
     const int tiles = a.M / kLoraTile + (a.N < a.M ? a.N : a.M);       // of adapters, at most
-    return lora::launch_dependent(lora::k_lora_join, tiles * (kLoraTile / lora::kJoinRows), lora::kJoinThreads, 0, s,
-                                  a);
+    return lora::launch_dependent(lora::k_lora_join, tiles * (kLoraTile / lora::join_rows(a.h_cols)),
+                                  lora::kJoinThreads, 0, s, a);
 }
 
 cudaError_t lora_shrink_set_attributes()
