@@ -1,8 +1,9 @@
 // Router: softmax top-k with route weights, balance loss and per-expert
 // counts, and the gradient of the logits (include/exl3.h, "router").
 //
-// A warp owns a row: lane l holds the logits of experts l, l + 32, ... in
-// registers, so the row is read once.  Forward: m = max l, s = sum exp(l - m),
+// A warp owns a row: lane l holds the logits of experts 2l, 2l + 1, 2l + 64, ...
+// in registers (pairs: half the loads, stores and conversions), so the row is
+// read once.  Forward: m = max l, s = sum exp(l - m),
 // p_e = exp(l_e - m) / s (kept as the pair: m + log s in fp32 would lose s for
 // large |m|); then topk rounds of a warp-wide maximum over order-preserving
 // integer keys, ties to the lower expert (Chooser).  Backward, with G_e = dL/dp_e
@@ -41,29 +42,72 @@ EXL3_DEV void store_float(void *p, size_t i, int dtype, float v)
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// A row of logits as it lies in memory, lane l: experts l + 32 i.
+// The expert of a lane's value i.
+EXL3_DEV int expert_of(int i) { return 64 * (i / 2) + 2 * (threadIdx.x & 31) + (i & 1); }
+
+// A row of logits as it lies in memory: V / 2 pairs a lane.
 template <int DT, int V>
 struct RawRow {
     using T = std::conditional_t<DT == EXL3_F32, float, uint16_t>;
-    T v[V];
+    using Pair = std::conditional_t<DT == EXL3_F32, float2, uint32_t>;
+    Pair v[V / 2];
     EXL3_DEV void load(const void *p, size_t row, int E)
     {
-        const int lane = threadIdx.x & 31;
-        const T *q = static_cast<const T *>(p) + row + lane;
+        const T *q = static_cast<const T *>(p) + row;
+        if ((E & 1) == 0) {                        // every pair is aligned and whole
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = lane + 32 * i < E ? q[32 * i] : T(0);
+            for (int i = 0; i < V / 2; i++)
+                v[i] = expert_of(2 * i) < E ? *reinterpret_cast<const Pair *>(q + expert_of(2 * i)) : Pair{};
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) {
+                const int e = expert_of(2 * i);
+                const T a = e < E ? q[e] : T(0), b = e + 1 < E ? q[e + 1] : T(0);
+                if constexpr (DT == EXL3_F32)
+                    v[i] = make_float2(a, b);
+                else
+                    v[i] = (uint32_t)a | (uint32_t)b << 16;
+            }
+        }
     }
     EXL3_DEV float get(int i) const
     {
-        if constexpr (DT == EXL3_F32)
-            return v[i];
-        else if constexpr (DT == EXL3_BF16)
-            return __uint_as_float((uint32_t)v[i] << 16);
-        else
-            return __half2float(__ushort_as_half(v[i]));
+        if constexpr (DT == EXL3_F32) {
+            return i & 1 ? v[i / 2].y : v[i / 2].x;
+        } else if constexpr (DT == EXL3_BF16) {
+            return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+        } else {
+            const __half2 h = *reinterpret_cast<const __half2 *>(&v[i / 2]);
+            return i & 1 ? __high2float(h) : __low2float(h);
+        }
     }
 };
+
+// The gradient of a row, rounded to the logits' type.
+template <int DT, int V>
+EXL3_DEV void store_row(void *p, size_t row, int E, const float (&d)[V])
+{
+    if ((E & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            if (expert_of(i) < E) {
+                if constexpr (DT == EXL3_F32) {
+                    *reinterpret_cast<float2 *>(static_cast<float *>(p) + row + expert_of(i)) = make_float2(d[i], d[i + 1]);
+                } else if constexpr (DT == EXL3_BF16) {
+                    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p) + row + expert_of(i)) =
+                        __floats2bfloat162_rn(d[i], d[i + 1]);
+                } else {
+                    *reinterpret_cast<__half2 *>(static_cast<__half *>(p) + row + expert_of(i)) =
+                        __floats2half2_rn(d[i], d[i + 1]);
+                }
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            if (expert_of(i) < E)
+                store_float(p, row + expert_of(i), DT, d[i]);
+    }
+}
 
 // Unsigned integers in the order of the logits, -0 as +0 and NaN as -inf.
 // 16-bit logits (as fp32) order by their upper 19 bits: the lower 13 bits take
@@ -106,10 +150,9 @@ struct Chooser<true, V> {                          // 16-bit logits: expert in t
     uint32_t k[V];
     EXL3_DEV void init(const float (&l)[V], int E)
     {
-        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            const int e = lane + 32 * i;
+            const int e = expert_of(i);
             k[i] = e < E ? (order_key(l[i]) & ~kExpertBits) | (kExpertBits - e) : 0u;
         }
         sort_network<V>([&](int a, int b) {
@@ -140,10 +183,9 @@ struct Chooser<false, V> {                         // fp32 logits: key and exper
     int e[V];
     EXL3_DEV void init(const float (&l)[V], int E)
     {
-        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            e[i] = lane + 32 * i;
+            e[i] = expert_of(i);
             k[i] = e[i] < E ? order_key(l[i]) : 0u;           // every logit's key is above 0
         }
         sort_network<V>([&](int a, int b) {
@@ -228,7 +270,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
         float l[V];
 #pragma unroll
         for (int i = 0; i < V; i++)
-            l[i] = lane + 32 * i < E ? raw.get(i) : -INFINITY;
+            l[i] = expert_of(i) < E ? raw.get(i) : -INFINITY;
         const bool ok = BAL && (!a.valid || a.valid[t] != 0);
         if (t + step < a.M)                        // the next row, one round of work ahead
             raw.load(a.logits, (size_t)(t + step) * E, E);
@@ -277,8 +319,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
     float *rows = sm + E + 1;
 #pragma unroll
     for (int i = 0; i < V; i++)
-        if (lane + 32 * i < E)
-            rows[warp * E + lane + 32 * i] = psum[i];
+        if (expert_of(i) < E)
+            rows[warp * E + expert_of(i)] = psum[i];
     if (lane == 0)
         atomicAdd(cnt + E, nvalid);
     __syncthreads();
@@ -387,11 +429,12 @@ constexpr int kBackWarps = 8;
 template <int DT, int V>
 __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs a)
 {
-    extern __shared__ float sm[];                  // [warps][E]: the row's gradients at chosen experts
+    extern __shared__ float sm[];                  // [warps][E, even]: the row's gradients at chosen experts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, k = a.topk;
-    float *at = sm + warp * E;
-    for (int e = lane; e < E; e += 32)
+    const int pitch = (E + 1) / 2 * 2;             // read in pairs
+    float *at = sm + warp * pitch;
+    for (int e = lane; e < pitch; e += 32)
         at[e] = 0.0f;
     __syncwarp();
     float g[V];                                    // balance gradient of p_e on valid rows
@@ -403,7 +446,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
         }
 #pragma unroll
         for (int i = 0; i < V; i++)
-            g[i] = a.counts && lane + 32 * i < E ? cg * (float)a.counts[lane + 32 * i] : 0.0f;
+            g[i] = a.counts && expert_of(i) < E ? cg * (float)a.counts[expert_of(i)] : 0.0f;
     }
     // one row's inputs, read a row ahead of their use
     struct Row {
@@ -451,35 +494,41 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
                 atomicAdd(at + r.id, add);         // distinct ids: one addend each
             __syncwarp();
         }
-        float p[V], own[V], pg = 0.0f;
+        float p[V], own[V], pg = 0.0f;             // absent experts: own = g = 0, nothing stored
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            p[i] = some ? __expf(r.raw.get(i) - r.st.x) * inv : 0.0f;
-            own[i] = a.d_rw && lane + 32 * i < E ? at[lane + 32 * i] : 0.0f;
+        for (int i = 0; i < V; i += 2) {
+            const float2 at2 = a.d_rw && expert_of(i) < E ? *reinterpret_cast<const float2 *>(at + expert_of(i))
+                                                          : make_float2(0.0f, 0.0f);
+            own[i] = at2.x;
+            own[i + 1] = at2.y;
+            p[i] = __expf(r.raw.get(i) - r.st.x) * inv;
+            p[i + 1] = __expf(r.raw.get(i + 1) - r.st.x) * inv;
         }
+        if (!some)                                 // a row of -inf only
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                p[i] = 0.0f;
+        const float on = r.bal ? 1.0f : 0.0f;
         if (a.renorm) {
 #pragma unroll
             for (int i = 0; i < V; i++)
-                pg = lane + 32 * i < E && r.bal ? fmaf(p[i], g[i], pg) : pg;
-            pg = warp_sum(pg);
+                pg = expert_of(i) < E ? fmaf(p[i], g[i], pg) : pg;
+            pg = warp_sum(pg) * on;
 #pragma unroll
             for (int i = 0; i < V; i++)
-                own[i] = fmaf(p[i], (r.bal ? g[i] : 0.0f) - pg, own[i]);
+                own[i] = fmaf(p[i], fmaf(on, g[i], -pg), own[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                own[i] += r.bal ? g[i] : 0.0f;
-                pg = lane + 32 * i < E ? fmaf(p[i], own[i], pg) : pg;
+                own[i] = fmaf(on, g[i], own[i]);
+                pg = expert_of(i) < E ? fmaf(p[i], own[i], pg) : pg;
             }
             pg = warp_sum(pg);
 #pragma unroll
             for (int i = 0; i < V; i++)
                 own[i] = p[i] * (own[i] - pg);
         }
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            if (lane + 32 * i < E)
-                store_float(a.d_logits, (size_t)t * E + lane + 32 * i, DT, own[i]);
+        store_row<DT, V>(a.d_logits, (size_t)t * E, E, own);
         if (a.d_rw) {
             __syncwarp();
             if (r.id >= 0)
@@ -523,7 +572,7 @@ cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
     const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 8;
     k_router_backward<DT, V>
-        <<<need < most ? need : most, kBackWarps * 32, (size_t)kBackWarps * a.E * 4, s>>>(a);
+        <<<need < most ? need : most, kBackWarps * 32, (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -532,8 +581,7 @@ template <int DT, typename F>
 cudaError_t by_width(int E, F f)
 {
     constexpr std::integral_constant<int, DT> dt;
-    const int v = (E + 31) / 32;
-    if (v <= 1) return f(dt, std::integral_constant<int, 1>());
+    const int v = (E + 63) / 64 * 2;
     if (v <= 2) return f(dt, std::integral_constant<int, 2>());
     if (v <= 4) return f(dt, std::integral_constant<int, 4>());
     if (v <= 6) return f(dt, std::integral_constant<int, 6>());
