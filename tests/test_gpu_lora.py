@@ -31,10 +31,24 @@ def _acc(K):
     return (K / 16 + 32) * 2.0 ** -23
 
 
+_PAD = 0
+
+
+@pytest.fixture(autouse=True, params=["few", "many"])
+def rows(request):
+    """Every test runs as written, and with 1100 more rows that have no adapter:
+    batches of more than 1024 rows take the tensor-core kernels."""
+    global _PAD
+    _PAD = 1100 if request.param == "many" else 0
+    yield request.param
+    _PAD = 0
+
+
 class Batch:
     """Rows with their adapters, and every buffer the calls take."""
 
-    def __init__(self, ids, ranks, fin, fout, dtype="bf16", seed=0, id64=False, max_rank=None, train=True):
+    def __init__(self, ids, ranks, fin, fout, dtype="bf16", seed=0, id64=False, max_rank=None, pad=None):
+        ids = np.concatenate([np.asarray(ids, np.int64), np.full(_PAD if pad is None else pad, -1, np.int64)])
         g = torch.Generator().manual_seed(seed)
         dt = _T[dtype]
 
@@ -150,6 +164,7 @@ def _plan_words(b):
 
 @pytest.mark.parametrize("M,N", [(0, 1), (1, 1), (5, 3), (33, 2), (1024, 7), (1025, 1024), (5000, 40), (40000, 300)])
 @pytest.mark.parametrize("id64", [False, True])
+@pytest.mark.parametrize("rows", ["few"], indirect=True)
 def test_plan_is_the_stable_grouping(M, N, id64):
     b = Batch.__new__(Batch)
     b.ids_np, b.M, b.N = _ids(M, N, M + N), M, N
@@ -173,7 +188,7 @@ SHAPES = [
     (1, [16], 128, 128), (1, [1], 5120, 1536), (2, [3, 128], 1408, 640), (7, [8, 5, 17], 256, 384),
     (16, [4], 384, 128), (17, [12, 64], 1536, 256), (40, [9] * 24, 640, 1408), (129, [16], 128, 2048),
     (130, [33, 2], 2048, 128), (300, [100, 1, 31, 64, 16], 1152, 896), (513, [128], 896, 1152),
-    (1000, [16, 16, 24], 640, 768),
+    (1000, [16, 16, 24], 640, 768), (1030, [64, 7], 384, 1664), (2500, [128, 48, 3], 512, 384),
 ]
 
 
@@ -185,7 +200,7 @@ def test_forward_and_backward(M, ranks, fin, fout, dtype):
     check(b)
 
 
-@pytest.mark.parametrize("M", [15, 16, 17, 127, 128, 129, 255, 257])
+@pytest.mark.parametrize("M", [7, 8, 9, 127, 128, 129, 255, 257, 1024, 1025, 1281])
 def test_one_adapter_at_tile_edges(M):
     check(Batch([0] * M, [24], 256, 256, "bf16", seed=M).all())
 
@@ -218,7 +233,7 @@ def test_rank_zero_changes_nothing():
 
 
 def test_empty_batch():
-    b = Batch([], [8, 3], 256, 128)
+    b = Batch([], [8, 3], 256, 128, pad=0)
     b.make_plan()
     b.forward()
     b.backward()
@@ -282,7 +297,7 @@ def test_nan_stays_in_its_row_and_adapter(M):
     b.forward()
     b.backward()
     torch.cuda.synchronize()
-    other = torch.ones(M, dtype=torch.bool)
+    other = torch.ones(b.M, dtype=torch.bool)
     other[1] = False
     assert torch.equal(b.y[other], clean.y[other]) and torch.equal(b.dx[other], clean.dx[other])
     assert not torch.isfinite(b.y[1]).any() and not torch.isfinite(b.dx[1]).any()
@@ -301,7 +316,7 @@ def test_nan_weights_stay_with_their_adapter():
     b.forward()
     b.backward()
     torch.cuda.synchronize()
-    other = torch.from_numpy(ids != 1)
+    other = torch.from_numpy(b.ids_np != 1)
     assert torch.equal(b.y[other], clean.y[other]) and torch.equal(b.dx[other], clean.dx[other])
     for a in (0, 2):
         assert torch.equal(b.dA[a], clean.dA[a]) and torch.equal(b.dB[a], clean.dB[a])
@@ -429,6 +444,7 @@ def test_entries_of_adapters_without_rows_are_not_read_forward():
 
 
 @pytest.mark.parametrize("wide", ["in", "out"])
+@pytest.mark.parametrize("rows", ["many"], indirect=True)
 def test_offsets_beyond_32_bits(wide):
     M, width = 430_000, 5120                            # 2.2e9 elements
     fin, fout = (width, 128) if wide == "in" else (128, width)
@@ -439,7 +455,7 @@ def test_offsets_beyond_32_bits(wide):
     dy = torch.zeros(M, fout, dtype=torch.float16, device="cuda")
     x[-5:] = torch.randn(5, fin, generator=g).half().cuda()
     dy[-5:] = torch.randn(5, fout, generator=g).half().cuda() * 0.1
-    s = Batch(ids[-5:], [8, 16], fin, fout, "f16", seed=1)
+    s = Batch(ids[-5:], [8, 16], fin, fout, "f16", seed=1, pad=0)
     s.x.copy_(x[-5:])
     s.dy.copy_(dy[-5:])
     plan = torch.empty(X.exl3_lora_plan_bytes(M, 2), dtype=torch.uint8, device="cuda")
