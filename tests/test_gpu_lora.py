@@ -225,6 +225,25 @@ def test_no_row_has_an_adapter():
     assert not any(g.any() for g in b.dA + b.dB)
 
 
+def test_idle_batches_after_failed_calls():
+    """A call of rows without adapters right after one whose tables were bad: no error is left over."""
+    good = Batch([-1] * 50, [8, 8], 256, 128)
+    bad = Batch([0, 1] * 25, [8, 8], 256, 128)
+    bad.ws = good.ws
+    good.make_plan()
+    bad.make_plan()
+    bad.ad.t_A[1] = 0
+    for _ in range(20):
+        bad.forward()
+        good.forward()
+        bad.backward()
+        good.backward()
+    torch.cuda.synchronize()
+    assert X.exl3_workspace_error(good.ws) == 0
+    assert torch.equal(good.y, good.base) and torch.equal(good.dx, good.dx_base)
+    assert not any(g.any() for g in good.dA + good.dB)
+
+
 def test_rank_zero_changes_nothing():
     b = Batch([0, 1, 1, 0, -1] * 30, [0, 8], 256, 128).all()
     check(b)
@@ -370,6 +389,28 @@ def test_same_bits_every_time_on_other_streams_and_in_a_graph(M):
     for rep in range(2):
         for t in b.outputs():
             t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, w) for s, w in zip(a.outputs(), b.outputs()))
+
+
+def test_graph_of_copies_and_calls():
+    """Calls captured right after copies and memsets."""
+    ids = _ids(70, 3, 5)
+    a = Batch(ids, [16, 8, 40], 384, 640, seed=8).all()
+    b = Batch(ids, [16, 8, 40], 384, 640, seed=8)
+    x, dy = b.x.clone(), b.dy.clone()
+    b.make_plan()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.x.copy_(x)
+        b.forward()
+        b.dy.copy_(dy)
+        b.dx.zero_()
+        b.backward()
+    for _ in range(2):
+        b.x.zero_()
+        b.dy.zero_()
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(s, w) for s, w in zip(a.outputs(), b.outputs()))

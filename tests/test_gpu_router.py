@@ -301,6 +301,25 @@ def test_graph_replay():
         assert torch.equal(getattr(c, n), getattr(want, n)), n
 
 
+def test_graph_of_copies_and_calls():
+    """Captured right after a copy and between memsets, as the first and the last node of a graph."""
+    z, src = _logits(90, 64, "f32", 2), _logits(90, 64, "f32", 3)
+    c = Call(z, 6, d_rw=torch.ones(90, 6, device="cuda"), d_loss=torch.ones(1, device="cuda"), backward=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        z.copy_(src)
+        c.go()
+        c.dl.zero_()
+        c.back()
+    want = Call(src, 6, d_rw=torch.ones(90, 6, device="cuda"), d_loss=torch.ones(1, device="cuda"), backward=True)
+    for _ in range(2):
+        z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for n in ("ids", "rw", "counts", "loss", "dl"):
+            assert torch.equal(getattr(c, n), getattr(want, n)), n
+
+
 def test_offsets_beyond_32_bits():
     M, E, k = 2_200_000, 1024, 2                       # 2.25e9 logits
     z = torch.zeros(M, E, dtype=torch.float16, device="cuda")

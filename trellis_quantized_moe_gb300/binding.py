@@ -126,7 +126,7 @@ def _ptr(t):
 
 
 def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _check(fn, rc, raise_on_error):
@@ -373,14 +373,17 @@ def exl3_router_forward(logits, ids, rw, renorm=False, stats=None, valid=None, c
     _shaped("logits", logits, (M, E))
     _shaped("ids", ids, (M, topk), torch.int32)
     _shaped("rw", rw, (M, topk))
-    _shaped("stats", stats, (M, 2), torch.float32)
-    _shaped("valid", valid, (M,), torch.uint8)
-    _shaped("counts", counts, (E + 1,), torch.int32)
-    _shaped("loss", loss, (1,), torch.float32)
-    rc = _lib.exl3_router_forward(_ptr(logits), _DTYPE[logits.dtype], M, E, topk, int(renorm),
-                                  _ptr(ids), _ptr(rw), _DTYPE[rw.dtype], _ptr(stats), _ptr(valid),
-                                  _ptr(counts), _ptr(loss), _ptr(workspace), _bytes(workspace),
-                                  _stream(stream))
+    if stats is not None:
+        _shaped("stats", stats, (M, 2), torch.float32)
+    if counts is not None or loss is not None:
+        _shaped("counts", counts, (E + 1,), torch.int32)
+        _shaped("loss", loss, (1,), torch.float32)
+    if valid is not None:
+        _shaped("valid", valid, (M,), torch.uint8)
+    rc = _lib.exl3_router_forward(logits.data_ptr(), _DTYPE[logits.dtype], M, E, topk, renorm,
+                                  ids.data_ptr(), rw.data_ptr(), _DTYPE[rw.dtype], _ptr(stats),
+                                  _ptr(valid), _ptr(counts), _ptr(loss), _ptr(workspace),
+                                  _bytes(workspace), _stream(stream))
     return _check("exl3_router_forward", rc, raise_on_error)
 
 
@@ -392,14 +395,18 @@ def exl3_router_backward(logits, ids, stats, d_logits, renorm=False, d_rw=None, 
     _shaped("ids", ids, (M, topk), torch.int32)
     _shaped("stats", stats, (M, 2), torch.float32)
     _shaped("d_logits", d_logits, (M, E), logits.dtype)
-    _shaped("d_rw", d_rw, (M, topk))
-    _shaped("valid", valid, (M,), torch.uint8)
-    _shaped("counts", counts, (E + 1,), torch.int32)
-    _shaped("d_loss", d_loss, (1,), torch.float32)
+    if d_rw is not None:
+        _shaped("d_rw", d_rw, (M, topk))
+    if valid is not None:
+        _shaped("valid", valid, (M,), torch.uint8)
+    if counts is not None or d_loss is not None:
+        _shaped("counts", counts, (E + 1,), torch.int32)
+        _shaped("d_loss", d_loss, (1,), torch.float32)
     rw_dtype = EXL3_F32 if d_rw is None else _DTYPE[d_rw.dtype]
-    rc = _lib.exl3_router_backward(_ptr(logits), _DTYPE[logits.dtype], M, E, topk, int(renorm),
-                                   _ptr(ids), _ptr(stats), _ptr(d_rw), rw_dtype, _ptr(valid),
-                                   _ptr(counts), _ptr(d_loss), _ptr(d_logits), _stream(stream))
+    rc = _lib.exl3_router_backward(logits.data_ptr(), _DTYPE[logits.dtype], M, E, topk, renorm,
+                                   ids.data_ptr(), stats.data_ptr(), _ptr(d_rw), rw_dtype,
+                                   _ptr(valid), _ptr(counts), _ptr(d_loss), d_logits.data_ptr(),
+                                   _stream(stream))
     return _check("exl3_router_backward", rc, raise_on_error)
 
 
@@ -414,29 +421,37 @@ def exl3_lora_plan(ids, N, plan, stream=None, raise_on_error=True) -> int:
 def exl3_lora_forward(x, plan, adapters: DeviceAdapters, y, workspace, base=None, h=None,
                       stream=None, raise_on_error=True) -> int:
     M, dt = x.shape[0], adapters.dtype
+    out = (M, adapters.out_features)
     _shaped("x", x, (M, adapters.in_features), dt)
-    _shaped("y", y, (M, adapters.out_features), dt)
-    _shaped("base", base, (M, adapters.out_features), dt)
-    _shaped("h", h, (M, adapters.h_cols), dt)
-    rc = _lib.exl3_lora_forward(_ptr(x), _DTYPE[dt], M, adapters._ref, _ptr(plan),
-                                _bytes(plan), _ptr(base), _ptr(y), _ptr(h), _ptr(workspace), _bytes(workspace),
-                                _stream(stream))
+    _shaped("y", y, out, dt)
+    if base is not None:
+        _shaped("base", base, out, dt)
+    if h is not None:
+        _shaped("h", h, (M, adapters.h_cols), dt)
+    rc = _lib.exl3_lora_forward(x.data_ptr(), _DTYPE[dt], M, adapters._ref, plan.data_ptr(),
+                                _bytes(plan), _ptr(base), y.data_ptr(), _ptr(h),
+                                workspace.data_ptr(), _bytes(workspace), _stream(stream))
     return _check("exl3_lora_forward", rc, raise_on_error)
 
 
 def exl3_lora_backward(dy, x, h, plan, adapters: DeviceAdapters, grads, workspace, dx=None,
                        dx_base=None, stream=None, raise_on_error=True) -> int:
     M, dt = dy.shape[0], adapters.dtype
+    inp = (M, adapters.in_features)
     _shaped("dy", dy, (M, adapters.out_features), dt)
-    _shaped("x", x, (M, adapters.in_features), dt)
-    _shaped("h", h, (M, adapters.h_cols), dt)
-    _shaped("dx", dx, (M, adapters.in_features), dt)
-    _shaped("dx_base", dx_base, (M, adapters.in_features), dt)
-    if grads is not None and (grads.ranks != adapters.ranks or grads.dtype != dt):
+    if x is not None:
+        _shaped("x", x, inp, dt)
+    if h is not None:
+        _shaped("h", h, (M, adapters.h_cols), dt)
+    if dx is not None:
+        _shaped("dx", dx, inp, dt)
+    if dx_base is not None:
+        _shaped("dx_base", dx_base, inp, dt)
+    if grads is not None and (grads.ranks != adapters.ranks or grads.dtype is not dt):
         raise ValueError("grads must hold a tensor like A and one like B for every adapter")
-    rc = _lib.exl3_lora_backward(_ptr(dy), _ptr(x), _ptr(h), _DTYPE[dt], M, adapters._ref,
-                                 _ptr(plan), _bytes(plan), _ptr(dx_base), _ptr(dx),
-                                 None if grads is None else grads._ref, _ptr(workspace),
+    rc = _lib.exl3_lora_backward(dy.data_ptr(), _ptr(x), _ptr(h), _DTYPE[dt], M, adapters._ref,
+                                 plan.data_ptr(), _bytes(plan), _ptr(dx_base), _ptr(dx),
+                                 None if grads is None else grads._ref, workspace.data_ptr(),
                                  _bytes(workspace), _stream(stream))
     return _check("exl3_lora_backward", rc, raise_on_error)
 

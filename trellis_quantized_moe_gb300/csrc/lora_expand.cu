@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             static_cast<uint4 *>(a.y)[i] = make_uint4(0, 0, 0, 0);
     };
     if (!plan_ok(a.plan, a.M, a.N)) {
+        grid_dep_wait();            // (waited for by the kernels after)
         zero_fill(tid);
         return;
     }

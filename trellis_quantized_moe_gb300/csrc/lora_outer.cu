@@ -114,14 +114,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     __shared__ Item start;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_launch();
-    if (!plan_ok(a.plan, a.M, a.N))
+    // (a CTA that has nothing to do waits too: the join takes this kernel's end
+    // for the end of the kernels before)
+    if (!plan_ok(a.plan, a.M, a.N)) {
+        grid_dep_wait();
         return;
+    }
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
     const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kOuterMin);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
-    if (begin >= end)
+    if (begin >= end) {
+        grid_dep_wait();
         return;
+    }
     const int sbytes = stage_bytes(a.h_cols), nslots = ring_slots(a.h_cols);
     volatile int *abort = &c.abort;
     if (warp == 0) {
@@ -331,8 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
 // other blocks zero the gradients of adapters without rows.
 __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs a)
 {
-    if (!plan_ok(a.plan, a.M, a.N))
+    if (!plan_ok(a.plan, a.M, a.N)) {
+        grid_dep_wait();
         return;
+    }
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *steps = a.plan + L.steps / 4;
     const int share = blockIdx.x / kJoinParts;

@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int ctas = a.ctas, all_warps = ctas * kWarps;
     const int cta = blockIdx.x % ctas, own = blockIdx.x / ctas;
-    grid_dep_launch();
+    grid_dep_wait();                // plan, tables and rows may come from the kernel before
+    grid_dep_launch();              // only now: the kernels after read the plan before their own wait
     auto zero_fill = [&]() {
         const size_t all = a.y ? (size_t)a.M * a.out_width / 8 : 0;
         for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < all; i += (size_t)gridDim.x * kThreads)
@@ -322,17 +323,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
 template <bool BF, int MT>
 cudaError_t launch(const LoraRowsArgs &a, int clusters, cudaStream_t s)
 {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = a.ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(clusters * a.ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = rows_smem<MT>();
     cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_lora_rows<BF, MT>, a);
 }
 

@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Ctl c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dep_launch();
+    grid_dep_wait();                // plan, tables and rows may come from the kernel before
+    grid_dep_launch();              // only now: the kernels after read them before their own wait
     if (blockIdx.x == 0 && warp == 14)
         check_tables(a);
     if (!plan_ok(a.plan, a.M, a.N))
@@ -271,13 +272,19 @@ EXL3_HD inline int join_rows(int h_cols) { return kJoinThreads / join_lanes(h_co
 __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
 {
     grid_dep_launch();
-    if (!plan_ok(a.plan, a.M, a.N))
+    // (a CTA that has nothing to do waits too: the kernel after this one takes
+    // its end for the end of the kernels before)
+    if (!plan_ok(a.plan, a.M, a.N)) {
+        grid_dep_wait();
         return;
+    }
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int rows = join_rows(a.h_cols), blocks = kLoraTile / rows;
     const int active = a.plan[kLpActive], tile = blockIdx.x / blocks;
-    if (tile >= active)
+    if (tile >= active) {
+        grid_dep_wait();
         return;
+    }
     const int4 t = reinterpret_cast<const int4 *>(a.plan + L.tiles / 4)[tile];
     const int rank = min(max(a.rank[t.x], 0), a.h_cols), rp = (rank + 15) / 16 * 16;
     const float alpha = a.scale_h ? a.scale[t.x] : 1.0f;
@@ -330,8 +337,7 @@ cudaError_t lora_shrink_set_attributes()
 cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s)
 {
     const int smem = lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols);
-    lora::k_lora_shrink<<<ctas, lora::kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return lora::launch_dependent(lora::k_lora_shrink, ctas, lora::kThreads, smem, s, a);
 }
 
 }  // namespace exl3

@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
     int32_t *cnt = reinterpret_cast<int32_t *>(sm);
     float psum[V];
     int nvalid = 0;
+    grid_dep_wait();                               // logits may come from the kernel before
+    grid_dep_launch();
     if (BAL) {
-        grid_dep_launch();
         for (int e = threadIdx.x; e <= E; e += blockDim.x)
             cnt[e] = 0;
 #pragma unroll
@@ -437,6 +438,8 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
     for (int e = lane; e < pitch; e += 32)
         at[e] = 0.0f;
     __syncwarp();
+    grid_dep_wait();                               // the inputs may come from the kernel before
+    grid_dep_launch();
     float g[V];                                    // balance gradient of p_e on valid rows
     {
         float cg = 0.0f;
@@ -538,6 +541,24 @@ __global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs 
     }
 }
 
+// Launches that may start while the kernel before them in the stream still
+// runs; each kernel waits for it before it reads anything.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int DT, int V>
 cudaError_t forward(const RouterArgs &a, cudaStream_t s)
 {
@@ -546,34 +567,20 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
         // few rows: a warp each on as many SMs as there are
         const int warps = a.M >= a.num_sms * kRouterWarps ? kRouterWarps : a.M >= 4 * a.num_sms ? 4 : 1;
         const int need = (a.M + warps - 1) / warps, most = a.num_sms * (64 / kRouterWarps) * (kRouterWarps / warps);
-        k_router_forward<DT, V, false><<<need < most ? need : most, warps * 32, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch(k_router_forward<DT, V, false>, need < most ? need : most, warps * 32, 0, s, a);
     }
     const int n = router_balance_ctas(a.M);
-    if (n > 0)
-        k_router_forward<DT, V, true><<<n, kRouterWarps * 32, bal_smem, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (n == 1 || e != cudaSuccess)
-        return e;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = n > 0;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kJoin);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_router_join, a, n);
+    const cudaError_t e =
+        n > 0 ? launch(k_router_forward<DT, V, true>, n, kRouterWarps * 32, bal_smem, s, a) : cudaSuccess;
+    return n == 1 || e != cudaSuccess ? e : launch(k_router_join, kJoin, kJoinThreads, 0, s, a, n);
 }
 
 template <int DT, int V>
 cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
     const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 8;
-    k_router_backward<DT, V>
-        <<<need < most ? need : most, kBackWarps * 32, (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_router_backward<DT, V>, need < most ? need : most, kBackWarps * 32,
+                  (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s, a);
 }
 
 // f(dtype, experts per lane) for the smallest instantiation that holds E experts.
