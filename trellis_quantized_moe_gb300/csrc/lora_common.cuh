@@ -113,6 +113,14 @@ EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
     return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;
 }
 
+// After a wait ran out: the MMAs issued so far end (waited for with a limit)
+// before their TMEM is freed.
+EXL3_DEV void drain_mmas(uint64_t *bar)
+{
+    mma_commit(bar);
+    mbar_wait(bar, 0);
+}
+
 // Launch that may start while the kernel before it in the stream still runs;
 // the kernel itself waits (grid_dep_wait) before it touches that one's results.
 template <typename Args>

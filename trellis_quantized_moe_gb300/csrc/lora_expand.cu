@@ -46,7 +46,8 @@ EXL3_HD inline Geom geom(int h_cols)
 EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
 
 struct Ctl {
-    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs];
+    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs],
+        drain;
     uint32_t tmem;
     int abort;
 };
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             mbar_init(&c.tfull[i], 1);
             mbar_init(&c.tempty[i], 256);
         }
+        mbar_init(&c.drain, 1);
         c.abort = 0;
         fence_mbar_init();
     }
@@ -303,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             mma_commit(&c.hempty[hb.slot]);
             hb.next(2);
         }
+        if (!ok)
+            drain_mmas(&c.drain);
     }
     fence_before();
     __syncthreads();

@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
     }
     // the second product's first weights and base rows, on their way during the reduction
     constexpr int kPre = MT < 4 ? MT : 4;
+    constexpr bool kAhead = MT <= 2;               // registers for two groups
     // (rows that only keep base need nothing when it is y already)
     const int groups = a.y && own < ntiles && (nmt > 0 || a.base != a.y) ? a.out_width / 64 : 0;
     const int first = warp * ctas + cta;
@@ -272,16 +273,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 acc[i][e] = 0.0f;
-        if (grp != first)
+        if (grp != first && !kAhead)
             load_base(grp, fb);
+        uint4 cur[kPre][4], cb[2] = {fb[0], fb[1]};
+#pragma unroll
+        for (int s = 0; s < kPre; s++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                cur[s][i] = pre[s][i];
+        if (kAhead && grp + all_warps < groups) {  // the next group's, while this one is worked on
+#pragma unroll
+            for (int s = 0; s < kPre; s++)
+                if (s < nmt)
+                    load_w2(s, grp + all_warps, pre[s]);
+            load_base(grp + all_warps, fb);
+        }
 #pragma unroll
         for (int s = 0; s < MT; s++)
             if (s < nmt) {
                 uint4 f[4];
-                if (s < kPre && grp == first) {
+                if (s < kPre && (kAhead || grp == first)) {
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        f[i] = pre[s < kPre ? s : 0][i];
+                        f[i] = cur[s < kPre ? s : 0][i];
                 } else {
                     load_w2(s, grp, f);
                 }
@@ -304,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
         for (int i = 0; i < 2; i++) {
             if (yrow[i] < 0)
                 continue;
-            uint4 u = fb[i];
+            uint4 u = cb[i];
             if (nmt > 0) {
                 uint32_t *pu = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll

@@ -32,7 +32,7 @@ EXL3_HD inline int ring_slots(int h_cols)
 }
 
 struct Ctl {
-    uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2];
+    uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort;
 };
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
             mbar_init(&c.tfull[i], 1);
             mbar_init(&c.tempty[i], 128);
         }
+        mbar_init(&c.drain, 1);
         c.abort = 0;
         fence_mbar_init();
     }
@@ -239,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
                 fresh = true;
             }
         }
+        if (!ok)
+            drain_mmas(&c.drain);
     } else if (warp == 13 && lane == 0) {
         // the proxy fence between the copies and the MMAs, off the MMA
         // thread's path (one thread, every stage in order: a thread that left

@@ -353,9 +353,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
 // the experts; 1024 / 32 = 32 threads per expert, whose parts are added in order.
 constexpr int kJoin = 8, kJoinThreads = 1024;
 
+EXL3_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+EXL3_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 EXL3_DEV void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_router_join(RouterArgs a, int n)
@@ -363,16 +366,10 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
     __shared__ float sp[kJoinThreads], scratch[32], parts[kJoin];
     __shared__ int sc[kJoinThreads];
     const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    cluster_sync();                                // CTA 0's shared memory may be written from here on
+    cluster_arrive();                              // CTA 0's shared memory may be written after the wait
     grid_dep_wait();
     // valid rows: a thread per CTA of the balance pass
-    int t = threadIdx.x < n ? a.pcount[(size_t)threadIdx.x * (E + 1) + E] : 0;
-    t = __reduce_add_sync(0xffffffffu, t);
-    if (lane == 0)
-        sc[warp] = t;
-    __syncthreads();
-    const int T = __reduce_add_sync(0xffffffffu, sc[lane]);
-    __syncthreads();
+    const int valid = threadIdx.x < n ? a.pcount[(size_t)threadIdx.x * (E + 1) + E] : 0;
     const int per = (E + kJoin - 1) / kJoin, e0 = blockIdx.x * per, e1 = min(E, e0 + per);
     float dot = 0.0f;
     for (int base = e0; base < e1; base += 32) {   // 32 experts at a time, 32 threads each
@@ -399,6 +396,7 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
         sc[threadIdx.x] = c;
         __syncthreads();
         if (warp == 0 && e < e1) {
+#pragma unroll
             for (int w = 1; w < 32; w++) {
                 p += sp[w * 32 + lane];
                 c += sc[w * 32 + lane];
@@ -409,6 +407,13 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
         __syncthreads();
     }
     dot = block_dot(dot, scratch);
+    if (blockIdx.x == 0) {
+        const int t = __reduce_add_sync(0xffffffffu, valid);
+        if (lane == 0)
+            sc[warp] = t;
+        __syncthreads();
+    }
+    cluster_wait();
     // every CTA's part into CTA 0 of the cluster
     if (threadIdx.x == 0) {
         uint32_t dst;
@@ -420,6 +425,9 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
         float v = 0.0f;
         for (int i = 0; i < kJoin; i++)
             v += parts[i];
+        int T = 0;
+        for (int i = 0; i < 32; i++)
+            T += sc[i];
         a.counts[E] = T;
         *a.loss = loss_of(a, v, T);
     }
