@@ -110,7 +110,7 @@ def _lb(ad=None, grads=None, **kw):
     (dict(x=None), NULL), (dict(dt=2), DTYPE), (dict(M=-1), SHAPE), (dict(ad=dict(N=0)), SHAPE),
     (dict(ad=dict(N=1025)), SHAPE), (dict(ad=dict(max_rank=0)), SHAPE),
     (dict(ad=dict(max_rank=129)), SHAPE), (dict(ad=dict(in_features=200)), SHAPE),
-    (dict(ad=dict(out_features=0)), SHAPE), (dict(ad=dict(A=P + 4)), ALIGN),
+    (dict(ad=dict(out_features=0)), SHAPE), (dict(M=1 << 29, ad=dict(in_features=1 << 20)), SHAPE), (dict(ad=dict(A=P + 4)), ALIGN),
     (dict(ad=dict(rank=P + 2)), ALIGN), (dict(plan=P + 16), ALIGN), (dict(ws=P + 128), ALIGN),
     (dict(x=P + 8), ALIGN), (dict(h=P + 2), ALIGN), (dict(wsb=64), WORKSPACE), (dict(pb=64), WORKSPACE),
 ])

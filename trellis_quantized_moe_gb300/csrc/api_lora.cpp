@@ -12,7 +12,8 @@ bool sizes_ok(int M, int N, int in_f, int out_f, int max_rank)
 {
     return M >= 0 && M < (1 << 30) && N >= 1 && N <= EXL3_MAX_ADAPTERS && in_f > 0 && out_f > 0 &&
            in_f % kHb == 0 && out_f % kHb == 0 && in_f < (1 << 24) && out_f < (1 << 24) && max_rank >= 1 &&
-           max_rank <= EXL3_MAX_RANK;
+           max_rank <= EXL3_MAX_RANK &&
+           ((long long)M / 64 + N) * ((in_f + out_f) / 64) < (1ll << 31);   // work items are counted in 32 bits
 }
 
 int check_adapters(const exl3_adapters *ad)

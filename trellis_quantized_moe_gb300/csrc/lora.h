@@ -55,6 +55,9 @@ constexpr int kShrinkMin = 4;        // stages below which a CTA is not worth it
 constexpr int kOuterK = 64;          // rows of one outer stage
 constexpr int kOuterN = 256;         // columns of one outer item
 constexpr int kOuterMin = 4;
+// Rows up to which an outer item is never cut: its at most eight stages take
+// less than the join kernel (300 rows: 7.6 us with it, see k_lora_outer).
+constexpr int kOuterWholeRows = 512;
 
 // `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).
 EXL3_HD inline int lora_share(int total, int ctas, int least)
@@ -154,6 +157,7 @@ struct LoraRowsArgs {
 struct LoraOuterArgs {
     const int32_t *plan;
     int M, N, act_dtype, h_cols, ctas;
+    int whole;                      // shares end at items' ends: no partials, no join kernel
     const int32_t *rank;
     const float *scale;
     struct Product {
@@ -171,7 +175,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s
 cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s);
-cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);
+cudaError_t launch_lora_outer(LoraOuterArgs a, cudaStream_t s);
 cudaError_t lora_plan_set_attributes();
 cudaError_t lora_shrink_set_attributes();
 cudaError_t lora_expand_set_attributes();
