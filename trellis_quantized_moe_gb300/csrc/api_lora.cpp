@@ -68,35 +68,37 @@ struct Products {
     void *y, *h;
 };
 
-cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_adapters *ad,
-                         const exl3_adapters *grads, const void *plan, void *ws, const LoraWsLayout &L, int sms,
-                         cudaStream_t stream)
+LoraRowsArgs rows_args(const Products &p, int act_dtype, int M, const exl3_adapters *ad, const exl3_adapters *grads,
+                       const void *plan, void *ws)
 {
-    const int ctas = product_ctas(sms);
-    if (M <= kRowsMax) {
-        LoraRowsArgs a{};
-        a.plan = static_cast<const int32_t *>(plan);
-        a.M = M;
-        a.N = ad->N;
-        a.act_dtype = act_dtype;
-        a.max_rank = ad->max_rank;
-        a.h_cols = lora_h_cols(ad->max_rank);
-        a.in_width = p.in_width;
-        a.out_width = p.out_width;
-        a.scale_h = p.scale_h;
-        a.x = p.x;
-        a.W1 = p.W1;
-        a.W2 = p.W2;
-        a.GA = grads ? grads->A : nullptr;
-        a.GB = grads ? grads->B : nullptr;
-        a.rank = ad->rank;
-        a.scale = ad->scale;
-        a.base = p.base;
-        a.y = p.y;
-        a.h = p.h;
-        a.hdr = static_cast<int32_t *>(ws);
-        return launch_lora_rows(a, sms, stream);
-    }
+    LoraRowsArgs a{};
+    a.plan = static_cast<const int32_t *>(plan);
+    a.M = M;
+    a.N = ad->N;
+    a.act_dtype = act_dtype;
+    a.max_rank = ad->max_rank;
+    a.h_cols = lora_h_cols(ad->max_rank);
+    a.in_width = p.in_width;
+    a.out_width = p.out_width;
+    a.scale_h = p.scale_h;
+    a.x = p.x;
+    a.W1 = p.W1;
+    a.W2 = p.W2;
+    a.GA = grads ? grads->A : nullptr;
+    a.GB = grads ? grads->B : nullptr;
+    a.rank = ad->rank;
+    a.scale = ad->scale;
+    a.base = p.base;
+    a.y = p.y;
+    a.h = p.h;
+    a.hdr = static_cast<int32_t *>(ws);
+    return a;
+}
+
+// The first product and its join.
+cudaError_t run_shrink(const Products &p, int act_dtype, int M, const exl3_adapters *ad, const exl3_adapters *grads,
+                       const void *plan, void *ws, const LoraWsLayout &L, int ctas, cudaStream_t stream)
+{
     LoraShrinkArgs sh{};
     sh.plan = static_cast<const int32_t *>(plan);
     sh.M = M;
@@ -114,7 +116,7 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
     sh.GA = grads ? grads->A : nullptr;
     sh.GB = grads ? grads->B : nullptr;
     sh.hdr = static_cast<int32_t *>(ws);
-    cudaError_t e = launch_lora_shrink(sh, ctas, stream);
+    const cudaError_t e = launch_lora_shrink(sh, ctas, stream);
     if (e != cudaSuccess)
         return e;
     LoraJoinArgs jn{};
@@ -131,15 +133,19 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
     jn.scale = ad->scale;
     jn.h = p.h;
     jn.hdr = sh.hdr;
-    e = launch_lora_join(jn, stream);
-    if (e != cudaSuccess || !p.y)
-        return e;
+    return launch_lora_join(jn, stream);
+}
+
+// The second product.
+cudaError_t run_expand(const Products &p, int act_dtype, int M, const exl3_adapters *ad, const void *plan, void *ws,
+                       int ctas, cudaStream_t stream)
+{
     LoraExpandArgs ex{};
-    ex.plan = sh.plan;
+    ex.plan = static_cast<const int32_t *>(plan);
     ex.M = M;
-    ex.N = sh.N;
+    ex.N = ad->N;
     ex.act_dtype = act_dtype;
-    ex.h_cols = sh.h_cols;
+    ex.h_cols = lora_h_cols(ad->max_rank);
     ex.width = p.out_width;
     ex.scale_h = p.scale_h;
     ex.h = p.h;
@@ -148,8 +154,25 @@ cudaError_t run_products(const Products &p, int act_dtype, int M, const exl3_ada
     ex.scale = ad->scale;
     ex.base = p.base;
     ex.y = p.y;
-    ex.hdr = sh.hdr;
+    ex.hdr = static_cast<int32_t *>(ws);
     return launch_lora_expand(ex, ctas, stream);
+}
+
+LoraOuterArgs outer_args(int act_dtype, int M, const exl3_adapters *ad, const void *plan, void *ws,
+                         const LoraWsLayout &L, int ctas)
+{
+    LoraOuterArgs o{};
+    o.plan = static_cast<const int32_t *>(plan);
+    o.M = M;
+    o.N = ad->N;
+    o.act_dtype = act_dtype;
+    o.h_cols = lora_h_cols(ad->max_rank);
+    o.ctas = ctas;
+    o.rank = ad->rank;
+    o.scale = ad->scale;
+    o.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
+    o.hdr = static_cast<int32_t *>(ws);
+    return o;
 }
 
 }  // namespace
@@ -223,9 +246,16 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
     const LoraWsLayout L = lora_ws_layout(M, ad->N, ad->in_features, ad->out_features, ad->max_rank);
     const Products p{x, ad->A, ad->B, ad->in_features, ad->out_features, 0, base, y,
                      h ? h : static_cast<uint8_t *>(ws) + L.h};
-    return run_products(p, act_dtype, M, ad, nullptr, plan, ws, L, sms, stream) == cudaSuccess
-               ? EXL3_OK
-               : EXL3_E_CUDA;
+    const int ctas = product_ctas(sms);
+    cudaError_t e;
+    if (M <= kRowsMax) {
+        e = launch_lora_rows(rows_args(p, act_dtype, M, ad, nullptr, plan, ws), sms, stream);
+    } else {
+        e = run_shrink(p, act_dtype, M, ad, nullptr, plan, ws, L, ctas, stream);
+        if (e == cudaSuccess)
+            e = run_expand(p, act_dtype, M, ad, plan, ws, ctas, stream);
+    }
+    return e == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }
 
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
@@ -262,24 +292,26 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
     const int ctas = product_ctas(sms);
     void *dh = static_cast<uint8_t *>(ws) + L.h;
     const Products p{dy, ad->B, ad->A, ad->out_features, ad->in_features, 1, dx_base, dx, dh};
-    if (run_products(p, act_dtype, M, ad, grads, plan, ws, L, sms, stream) != cudaSuccess)
-        return EXL3_E_CUDA;
-    if (!grads)
-        return EXL3_OK;
-    LoraOuterArgs o{};
-    o.plan = static_cast<const int32_t *>(plan);
-    o.M = M;
-    o.N = ad->N;
-    o.act_dtype = act_dtype;
-    o.h_cols = lora_h_cols(ad->max_rank);
-    o.ctas = ctas;
-    o.rank = ad->rank;
-    o.scale = ad->scale;
-    o.p[0] = {x, dh, grads->A, ad->in_features, 0};
-    o.p[1] = {dy, h, grads->B, ad->out_features, 1};
-    o.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.part);
-    o.hdr = static_cast<int32_t *>(ws);
-    return launch_lora_outer(o, stream) == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
+    LoraOuterArgs o = outer_args(act_dtype, M, ad, plan, ws, L, ctas);
+    if (grads) {
+        o.p[0] = {x, dh, grads->A, ad->in_features, 0};
+        o.p[1] = {dy, h, grads->B, ad->out_features, 1};
+    }
+    cudaError_t e;
+    if (M <= kRowsMax) {
+        e = launch_lora_rows(rows_args(p, act_dtype, M, ad, grads, plan, ws), sms, stream);
+        if (e == cudaSuccess && grads)
+            e = launch_lora_outer(o, stream);
+    } else {
+        // the weights' gradients first, while dy is in L2 (8192 rows, ranks 64
+        // and 128: 1 us)
+        e = run_shrink(p, act_dtype, M, ad, grads, plan, ws, L, ctas, stream);
+        if (e == cudaSuccess && grads)
+            e = launch_lora_outer(o, stream);
+        if (e == cudaSuccess && dx)
+            e = run_expand(p, act_dtype, M, ad, plan, ws, ctas, stream);
+    }
+    return e == cudaSuccess ? EXL3_OK : EXL3_E_CUDA;
 }
 
 }  // extern "C"

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         // h of each tile, K-major: rp / 8 chunks a row
         const int ht = tid - kHWarp * 32;
         Ring hb;
-        grid_dep_wait();                           // h comes from the kernel before
+        grid_dep_wait();                           // h comes from the kernels before
         for (int s = begin; s < end;) {
             const int tile = s / nb;
             const int4 t = tiles[tile];

@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
 // other blocks zero the gradients of adapters without rows.
 __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs a)
 {
+    grid_dep_launch();
     if (!plan_ok(a.plan, a.M, a.N)) {
         grid_dep_wait();
         return;

@@ -436,7 +436,7 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
 constexpr int kBackWarps = 8;
 
 template <int DT, int V>
-__global__ void __launch_bounds__(kBackWarps * 32) k_router_backward(RouterArgs a)
+__global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 5 : 1) k_router_backward(RouterArgs a)
 {
     extern __shared__ float sm[];                  // [warps][E, even]: the row's gradients at chosen experts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -586,7 +586,7 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
 template <int DT, int V>
 cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
-    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 8;
+    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * (V <= 6 ? 5 : 4);     // one wave
     return launch(k_router_backward<DT, V>, need < most ? need : most, kBackWarps * 32,
                   (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s, a);
 }
