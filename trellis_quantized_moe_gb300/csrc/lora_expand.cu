@@ -13,6 +13,12 @@
 // bulk copy per 256-byte row, in and out, took 38 cycles a copy: 5 us an item.)
 // NW = 128 for ranks up to 64, 64 above: the slots of a ring deep enough to
 // keep HBM busy must fit beside two 32 KB buffers of h.
+//
+// Measured: 16384 rows, 1536 outputs, rank 16: 19.5 us for 100 MB read and
+// written (5.1 TB/s; 15.4 us at the copy rate, most of the rest before the
+// first item ends); 8192 rows, 5120 outputs, ranks 64 and 128: 38 us for
+// 168 MB, at 5.9 TB/s between the first item and the last.  Four epilogue
+// warps instead of eight took 1.9 us an item instead of 1.
 #include "lora_common.cuh"
 
 namespace exl3 {

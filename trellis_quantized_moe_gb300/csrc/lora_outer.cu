@@ -12,6 +12,11 @@
 // every time).  The rows come in as they lie in memory: both MMA operands are
 // MN-major (x^T gives the 128 accumulator lanes, h the columns), so nothing is
 // transposed.
+//
+// Measured: 8192 rows, 5120 and 1536 columns, ranks 64 and 128: 29 us for 109 MB,
+// 0.85 us a stage (5.7 TB/s of x and dy, as much again of h from L2), then 8.6
+// us to join 40 MB of partials.  300 rows, 4096 and 1408 columns, rank 8, items
+// uncut: 7 us after the kernel before (cut, with the join: 9).
 #include "lora_common.cuh"
 
 namespace exl3 {

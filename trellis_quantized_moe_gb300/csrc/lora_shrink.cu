@@ -11,6 +11,12 @@
 // by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring by two
 // groups of loader warps that take turns; one thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
 // warps drain the accumulator, double-buffered in TMEM.
+//
+// Measured: 16384 rows x 5120 bf16, rank 16: 36 us for 168 MB (4.7 TB/s); the
+// same gathered copies through a ring without MMAs take 28.8.  Once running it
+// holds 5.9 TB/s; the rest is the start (plan, tile, rows, first bytes one
+// after the other: 5 us) and CTAs that end up to 4 us apart.  8192 rows, rank
+// 128: 26 us, W through L2 adding as many bytes per stage as x.
 #include "lora_common.cuh"
 
 namespace exl3 {

@@ -14,7 +14,9 @@
 // w_i (d_i - sum_j w_j d_j) at the chosen experts.
 //
 // What bounds it: not HBM but the instructions per row, most of them the
-// choice's.
+// choice's.  Measured at 65536 x 192 bf16, top 8: forward with the balance 30 us
+// (371 instructions a row, the ALU pipe 68% busy, DRAM 9%), join 5 us, backward
+// 22 us (293 instructions a row).
 #include <type_traits>
 
 #include "common.cuh"
@@ -148,46 +150,64 @@ struct Chooser;
 template <int V>
 struct Chooser<true, V> {                          // 16-bit logits: expert in the key
     uint32_t k[V];
+    template <bool FULL>
     EXL3_DEV void init(const float (&l)[V], int E)
     {
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int e = expert_of(i);
-            k[i] = e < E ? (order_key(l[i]) & ~kExpertBits) | (kExpertBits - e) : 0u;
+            k[i] = FULL || e < E ? (order_key(l[i]) & ~kExpertBits) | (kExpertBits - e) : 0u;
         }
+    }
+    EXL3_DEV void sort()
+    {
         sort_network<V>([&](int a, int b) {
             const uint32_t hi = max(k[a], k[b]), lo = min(k[a], k[b]);
             k[a] = hi;
             k[b] = lo;
         });
     }
-    // this round's choice, kept by lane j
-    EXL3_DEV void next(int j, uint32_t &mine, int &)
+    // this round's choice: the owner leaves it in out[j]
+    EXL3_DEV uint32_t next(int j, uint2 *out)
     {
         const uint32_t b = __reduce_max_sync(0xffffffffu, k[0]);
         const bool own = k[0] == b;
+        if (own)
+            out[j].x = b;
 #pragma unroll
         for (int i = 0; i + 1 < V; i++)
             k[i] = own ? k[i + 1] : k[i];
         k[V - 1] = own ? 0u : k[V - 1];
-        mine = (threadIdx.x & 31) == j ? b : mine;
+        return b;
     }
     // a negative logit's key has ones where the fraction ends
     static EXL3_DEV uint32_t key(uint32_t b) { return b & 0x80000000u ? b & ~kExpertBits : b | kExpertBits; }
-    static EXL3_DEV int expert(uint32_t b, int) { return kExpertBits - (b & kExpertBits); }
+    // lane j < topk: round j's choice
+    EXL3_DEV uint2 collect(int topk, const uint2 *out) const
+    {
+        __syncwarp();
+        const int lane = threadIdx.x & 31;
+        const uint32_t b = lane < topk ? out[lane].x : 0u;
+        __syncwarp();                              // read before the next row's are written
+        return make_uint2(b, kExpertBits - (b & kExpertBits));
+    }
 };
 
 template <int V>
 struct Chooser<false, V> {                         // fp32 logits: key and expert side by side
-    uint32_t k[V];
-    int e[V];
+    uint32_t k[V], mine = 0;
+    int e[V], id = 0;
+    template <bool FULL>
     EXL3_DEV void init(const float (&l)[V], int E)
     {
 #pragma unroll
         for (int i = 0; i < V; i++) {
             e[i] = expert_of(i);
-            k[i] = e[i] < E ? order_key(l[i]) : 0u;           // every logit's key is above 0
+            k[i] = FULL || e[i] < E ? order_key(l[i]) : 0u;   // every logit's key is above 0
         }
+    }
+    EXL3_DEV void sort()
+    {
         sort_network<V>([&](int a, int b) {
             const bool x = k[a] < k[b] || (k[a] == k[b] && e[a] > e[b]);
             const uint32_t ka = k[a];
@@ -198,7 +218,9 @@ struct Chooser<false, V> {                         // fp32 logits: key and exper
             e[b] = x ? ea : e[b];
         });
     }
-    EXL3_DEV void next(int j, uint32_t &mine, int &id)
+    // this round's choice, kept by lane j (through shared memory, as above, the
+    // longer rounds of this type were slower)
+    EXL3_DEV uint32_t next(int j, uint2 *)
     {
         const uint32_t b = __reduce_max_sync(0xffffffffu, k[0]);
         const int x = __reduce_min_sync(0xffffffffu, k[0] == b ? e[0] : 0x7FFFFFFF);
@@ -211,9 +233,10 @@ struct Chooser<false, V> {                         // fp32 logits: key and exper
             e[i] = own ? e[i + 1] : e[i];
         }
         k[V - 1] = own ? 0u : k[V - 1];
+        return b;
     }
     static EXL3_DEV uint32_t key(uint32_t b) { return b; }
-    static EXL3_DEV int expert(uint32_t, int id) { return id; }
+    EXL3_DEV uint2 collect(int, const uint2 *) const { return make_uint2(mine, id); }
 };
 
 // counts, T and loss from one expert's totals per thread: thread e of the CTA
@@ -243,10 +266,11 @@ EXL3_DEV float loss_of(const RouterArgs &a, float dot, int T)
 // leaves its own in the workspace (rows are dealt to warps in a fixed way and
 // everything is added in a fixed order), or finishes alone (one CTA).
 template <int DT, int V, bool BAL>
-__global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs a)
+__global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_forward(RouterArgs a)
 {
     extern __shared__ float sm[];                  // BAL: [E + 1] counts, then [warps][E] sums
     __shared__ float scratch[32];
+    __shared__ uint2 chosen[kRouterWarps][EXL3_ROUTER_MAX_TOPK];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int E = a.E, k = a.topk;
     int32_t *cnt = reinterpret_cast<int32_t *>(sm);
@@ -269,19 +293,26 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
         raw.load(a.logits, (size_t)t * E, E);
     for (; t < a.M; t += step) {
         float l[V];
+        using C = Chooser<DT != EXL3_F32, V>;
+        C choose;
+        if (E == 32 * V) {                         // no absent experts
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            l[i] = expert_of(i) < E ? raw.get(i) : -INFINITY;
+            for (int i = 0; i < V; i++)
+                l[i] = raw.get(i);
+            choose.template init<true>(l, E);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                l[i] = expert_of(i) < E ? raw.get(i) : -INFINITY;
+            choose.template init<false>(l, E);
+        }
+        choose.sort();
         const bool ok = BAL && (!a.valid || a.valid[t] != 0);
         if (t + step < a.M)                        // the next row, one round of work ahead
             raw.load(a.logits, (size_t)(t + step) * E, E);
-        using C = Chooser<DT != EXL3_F32, V>;
-        C choose;
-        choose.init(l, E);
-        uint32_t mine = 0;
-        int id = 0;
-        choose.next(0, mine, id);                  // the first choice has the largest logit
-        const float m = key_logit(C::key(__shfl_sync(0xffffffffu, mine, 0)));
+        uint2 *out = chosen[warp];
+        // the first choice has the largest logit
+        const float m = key_logit(C::key(choose.next(0, out)));
         const float ref = m == -INFINITY ? 0.0f : m;
         float s = 0.0f;
 #pragma unroll
@@ -299,10 +330,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_router_forward(RouterArgs
             for (int i = 0; i < V; i++)
                 psum[i] = fmaf(l[i], inv, psum[i]);
         }
+#pragma unroll 4
         for (int j = 1; j < k; j++)
-            choose.next(j, mine, id);
-        id = C::expert(mine, id);
-        float w = lane < k ? __expf(key_logit(C::key(mine)) - ref) * inv : 0.0f;
+            choose.next(j, out);
+        const uint2 mine = choose.collect(k, out);
+        const int id = (int)mine.y;
+        float w = lane < k ? __expf(key_logit(C::key(mine.x)) - ref) * inv : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(w);
             w = total == 0.0f ? 0.0f : w / total;
@@ -436,7 +469,7 @@ __global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(kJoinThreads) k_
 constexpr int kBackWarps = 8;
 
 template <int DT, int V>
-__global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 5 : 1) k_router_backward(RouterArgs a)
+__global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 4 : 1) k_router_backward(RouterArgs a)
 {
     extern __shared__ float sm[];                  // [warps][E, even]: the row's gradients at chosen experts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -505,10 +538,11 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 5 : 1) k_router_back
                 atomicAdd(at + r.id, add);         // distinct ids: one addend each
             __syncwarp();
         }
+        const bool full = E == 32 * V;
         float p[V], own[V], pg = 0.0f;             // absent experts: own = g = 0, nothing stored
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            const float2 at2 = a.d_rw && expert_of(i) < E ? *reinterpret_cast<const float2 *>(at + expert_of(i))
+        for (int i = 0; i < V; i += 2) {           // (at has room for a last pair, and absent pairs read none)
+            const float2 at2 = a.d_rw && (full || expert_of(i) < E) ? *reinterpret_cast<const float2 *>(at + expert_of(i))
                                                           : make_float2(0.0f, 0.0f);
             own[i] = at2.x;
             own[i + 1] = at2.y;
@@ -523,7 +557,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 5 : 1) k_router_back
         if (a.renorm) {
 #pragma unroll
             for (int i = 0; i < V; i++)
-                pg = expert_of(i) < E ? fmaf(p[i], g[i], pg) : pg;
+                pg = full || expert_of(i) < E ? fmaf(p[i], g[i], pg) : pg;
             pg = warp_sum(pg) * on;
 #pragma unroll
             for (int i = 0; i < V; i++)
@@ -532,7 +566,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 5 : 1) k_router_back
 #pragma unroll
             for (int i = 0; i < V; i++) {
                 own[i] = fmaf(on, g[i], own[i]);
-                pg = expert_of(i) < E ? fmaf(p[i], own[i], pg) : pg;
+                pg = full || expert_of(i) < E ? fmaf(p[i], own[i], pg) : pg;
             }
             pg = warp_sum(pg);
 #pragma unroll
@@ -586,7 +620,7 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
 template <int DT, int V>
 cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
-    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * (V <= 6 ? 5 : 4);     // one wave
+    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 4;     // one wave
     return launch(k_router_backward<DT, V>, need < most ? need : most, kBackWarps * 32,
                   (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s, a);
 }
