@@ -316,7 +316,8 @@ size_t exl3_lora_workspace_bytes(int M, int N, int in_features, int out_features
 
 /* x: [M][in]; base: [M][out] or NULL (zero), may be y; y: [M][out]; all
  *   act_dtype (f16/bf16).  h: act_dtype [M][exl3_lora_h_cols(max_rank)] or
- *   NULL: what the backward pass needs, rows in plan order. */
+ *   NULL: what the backward pass needs, rows in plan order.  plan_bytes: size of
+ *   the plan buffer, at least exl3_lora_plan_bytes(M, N). */
 int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *ad,
                       const void *plan, size_t plan_bytes, const void *base, void *y, void *h,
                       void *workspace, size_t ws_bytes, cudaStream_t stream);
@@ -326,7 +327,9 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
  *   A and B point at the outputs dA [rank][in] and dB [rank][out]; its rank and
  *   scale are not read), or NULL: not wanted; every adapter's gradients are
  *   written, zeros for one without rows.  At least one of dx, grads is needed.
- *   Sums over rows run in a fixed order: the same call gives the same bits. */
+ *   Sums over rows run in a fixed order: the same call gives the same bits.
+ *   A call that sets the error word (a bad plan or table entry) zero-fills y
+ *   or dx and writes no gradients. */
 int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dtype, int M,
                        const exl3_adapters *ad, const void *plan, size_t plan_bytes,
                        const void *dx_base, void *dx,

@@ -205,6 +205,16 @@ def test_one_adapter_at_tile_edges(M):
     check(Batch([0] * M, [24], 256, 256, "bf16", seed=M).all())
 
 
+@pytest.mark.parametrize("M,N", [(60, 1024), (900, 700), (1500, 1024)])
+def test_many_adapters(M, N):
+    rng = np.random.default_rng(M)
+    ranks = [int(r) for r in rng.integers(0, 20, N)]
+    b = Batch(_ids(M, N, M), ranks, 128, 256, "f16", seed=M, max_rank=20).all()
+    check(b)
+    used = set(b.ids_np.tolist())
+    assert all(not b.dA[a].any() and not b.dB[a].any() for a in range(N) if a not in used)
+
+
 def test_long_contiguous_requests():
     rng = np.random.default_rng(3)
     ids = np.repeat([2, -1, 0, 2, 1, -1], [400, 30, 700, 129, 1, 60])

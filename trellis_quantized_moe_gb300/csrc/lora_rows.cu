@@ -8,8 +8,9 @@
 // eight rows of one adapter.  Its warps share the contraction of the first
 // product in 32-wide blocks; the partial h are added warp by warp in
 // shared memory, then CTA by CTA over distributed shared memory (a fixed
-// order), so every CTA has h and goes on with its own columns of the second
-// product, whose weights and base rows are already on their way.
+// order) and rounded once to the operand type, so every CTA has h and goes on
+// with its own columns of the second product, whose weights and base rows are
+// already on their way.
 //
 // Operands go from global memory to mma.sync fragments directly, 16 bytes a
 // lane.  First product (M = ranks, N = rows): a lane's eight consecutive k

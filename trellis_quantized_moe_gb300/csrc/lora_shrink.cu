@@ -8,9 +8,10 @@
 // split over its width, one of many is not); a tile cut by the shares leaves
 // one fp32 partial per CTA, which k_lora_join adds in CTA order.  A stage
 // is 128 rows x 256 bytes of x and the adapter's rank x 256 bytes of W, copied
-// by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring by two
-// groups of loader warps that take turns; one thread issues tcgen05.mma (M = 128 rows, N = rank rounded up to 16), four
-// warps drain the accumulator, double-buffered in TMEM.
+// by cp.async (gathered rows: sixteen lanes per 256 bytes of a row) into a ring
+// by two groups of loader warps that take turns; one thread issues tcgen05.mma
+// (M = 128 rows, N = rank rounded up to 16), four warps drain the accumulator,
+// double-buffered in TMEM.
 //
 // Measured: 16384 rows x 5120 bf16, rank 16: 36 us for 168 MB (4.7 TB/s); the
 // same gathered copies through a ring without MMAs take 28.8.  Once running it
