@@ -264,7 +264,8 @@ int exl3_router_forward(const void *logits, int logits_dtype, int M, int E, int 
  *   the device, gradient of loss (with counts; both NULL: none).  Counts are
  *   constants of the loss; the gradient goes through P.  At least one of d_rw
  *   and d_loss is needed.  d_logits: [M][E] logits_dtype, and may be logits.
- *   An id outside [0, E) contributes nothing. */
+ *   An id outside [0, E) contributes nothing; a row's ids are distinct, as the
+ *   forward pass gives them. */
 int exl3_router_backward(const void *logits, int logits_dtype, int M, int E, int topk, int renorm,
                          const int32_t *ids, const float *stats, const void *d_rw, int rw_dtype,
                          const uint8_t *valid, const int32_t *counts, const float *d_loss,

@@ -44,6 +44,16 @@ EXL3_DEV void store_float(void *p, size_t i, int dtype, float v)
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x, to about two ulps; 0 below the normal range.
+EXL3_DEV float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The expert of a lane's value i.
 EXL3_DEV int expert_of(int i) { return 64 * (i / 2) + 2 * (threadIdx.x & 31) + (i & 1); }
 
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_f
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            l[i] = __expf(l[i] - ref);
+            l[i] = exp2_approx((l[i] - ref) * kLog2e);
             s += l[i];
         }
         s = warp_sum(s);
@@ -335,7 +345,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_f
             choose.next(j, out);
         const uint2 mine = choose.collect(k, out);
         const int id = (int)mine.y;
-        float w = lane < k ? __expf(key_logit(C::key(mine.x)) - ref) * inv : 0.0f;
+        float w = lane < k ? exp2_approx((key_logit(C::key(mine.x)) - ref) * kLog2e) * inv : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(w);
             w = total == 0.0f ? 0.0f : w / total;
@@ -500,80 +510,100 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 4 : 1) k_router_back
         int id;
         bool bal;
     } next;
+    const int step = gridDim.x * kBackWarps;
+    int t = blockIdx.x * kBackWarps + warp;
+    size_t at_next = (size_t)t * E, choice = (size_t)t * k + lane;       // of the row fetched next
+    const size_t row_step = (size_t)step * E, choice_step = (size_t)step * k;
     auto fetch = [&](int t, Row &r) {
-        r.raw.load(a.logits, (size_t)t * E, E);
+        r.raw.load(a.logits, at_next, E);
         r.st = reinterpret_cast<const float2 *>(a.stats)[t];
         r.bal = a.counts && (!a.valid || a.valid[t] != 0);
         r.id = -1;
         r.d = r.chosen = 0.0f;
         if (a.d_rw && lane < k) {
-            r.id = a.ids[(size_t)t * k + lane];
-            r.d = load_act(a.d_rw, (size_t)t * k + lane, a.rw_dtype);
+            r.id = a.ids[choice];
+            r.d = load_act(a.d_rw, choice, a.rw_dtype);
             if ((unsigned)r.id >= (unsigned)E)
                 r.id = -1;
             else if (a.renorm)
-                r.chosen = load_act(a.logits, (size_t)t * E + r.id, DT);
+                r.chosen = load_act(a.logits, at_next + r.id, DT);
         }
+        at_next += row_step;
+        choice += choice_step;
     };
-    const int step = gridDim.x * kBackWarps;
-    int t = blockIdx.x * kBackWarps + warp;
+    const bool full = E == 32 * V;                 // no absent experts
+    size_t here = at_next;
     if (t < a.M)
         fetch(t, next);
-    for (; t < a.M; t += step) {
+    for (; t < a.M; t += step, here += row_step) {
         const Row r = next;
         if (t + step < a.M)
             fetch(t + step, next);
-        const float inv = r.st.y == 0.0f ? 0.0f : __fdividef(1.0f, r.st.y);
-        const bool some = r.st.y != 0.0f;
+        const bool some = r.st.y != 0.0f;          // else a row of -inf only: p = 0
         if (a.d_rw) {
             float add = r.d;
             if (a.renorm) {                        // w_j (d_j - sum w d), beside the softmax's own term
-                const float pj = r.id >= 0 && some ? __expf(r.chosen - r.st.x) * inv : 0.0f;
+                const float pj = r.id >= 0 && some ? exp2_approx((r.chosen - r.st.x) * kLog2e - __log2f(r.st.y)) : 0.0f;
                 const float total = warp_sum(pj);
                 const float w = total == 0.0f ? 0.0f : pj / total;
                 const float wd = warp_sum(r.id >= 0 ? w * r.d : 0.0f);
                 add = w * (r.d - wd);
             }
             if (r.id >= 0)
-                atomicAdd(at + r.id, add);         // distinct ids: one addend each
+                at[r.id] = add;
             __syncwarp();
         }
-        const bool full = E == 32 * V;
-        float p[V], own[V], pg = 0.0f;             // absent experts: own = g = 0, nothing stored
+        // p = exp(l - m) / s = 2^((l - m) log2 e - log2 s)
+        const float ls = -__log2f(r.st.y);
+        float p[V], own[V];                        // absent experts: nothing stored, not in any sum
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {           // (at has room for a last pair, and absent pairs read none)
-            const float2 at2 = a.d_rw && (full || expert_of(i) < E) ? *reinterpret_cast<const float2 *>(at + expert_of(i))
-                                                          : make_float2(0.0f, 0.0f);
+        for (int i = 0; i < V; i += 2) {
+            const float2 at2 = a.d_rw && (full || expert_of(i) < E)
+                                   ? *reinterpret_cast<const float2 *>(at + expert_of(i))
+                                   : make_float2(0.0f, 0.0f);
             own[i] = at2.x;
             own[i + 1] = at2.y;
-            p[i] = __expf(r.raw.get(i) - r.st.x) * inv;
-            p[i + 1] = __expf(r.raw.get(i + 1) - r.st.x) * inv;
+            p[i] = exp2_approx(fmaf(r.raw.get(i) - r.st.x, kLog2e, ls));
+            p[i + 1] = exp2_approx(fmaf(r.raw.get(i + 1) - r.st.x, kLog2e, ls));
         }
-        if (!some)                                 // a row of -inf only
+        if (!some)
 #pragma unroll
             for (int i = 0; i < V; i++)
                 p[i] = 0.0f;
-        const float on = r.bal ? 1.0f : 0.0f;
-        if (a.renorm) {
+        // sum of p_e x_e over the row's experts
+        auto expectation = [&](const float (&x)[V]) {
+            float v = 0.0f;
+            if (full) {
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                pg = full || expert_of(i) < E ? fmaf(p[i], g[i], pg) : pg;
-            pg = warp_sum(pg) * on;
+                for (int i = 0; i < V; i++)
+                    v = fmaf(p[i], x[i], v);
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                own[i] = fmaf(p[i], fmaf(on, g[i], -pg), own[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                own[i] = fmaf(on, g[i], own[i]);
-                pg = full || expert_of(i) < E ? fmaf(p[i], own[i], pg) : pg;
+                for (int i = 0; i < V; i++)
+                    v = expert_of(i) < E ? fmaf(p[i], x[i], v) : v;
             }
-            pg = warp_sum(pg);
+            return warp_sum(v);
+        };
+        if (!a.renorm) {
+            if (r.bal)
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    own[i] += g[i];
+            const float pg = expectation(own);
 #pragma unroll
             for (int i = 0; i < V; i++)
                 own[i] = p[i] * (own[i] - pg);
+        } else if (r.bal) {
+            const float pg = expectation(g);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                own[i] = fmaf(p[i], g[i] - pg, own[i]);
+        } else {                                   // a NaN row stays one
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                own[i] = fmaf(p[i], 0.0f, own[i]);
         }
-        store_row<DT, V>(a.d_logits, (size_t)t * E, E, own);
+        store_row<DT, V>(a.d_logits, here, E, own);
         if (a.d_rw) {
             __syncwarp();
             if (r.id >= 0)
