@@ -278,8 +278,9 @@ int exl3_router_backward(const void *logits, int logits_dtype, int M, int E, int
  * y_t = base_t for rows without an adapter.  Backward:
  *   dh_t = scale_a * (B_a dy_t),  dx_t = dx_base_t + dh_t A_a,
  *   dA_a = sum_t dh_t x_t^T,  dB_a = scale_a * sum_t h_t dy_t^T.
- * Products accumulate in fp32; h and dh are rounded once to the activation
- * dtype (they are operands of the second product), every output once. */
+ * Products accumulate in fp32; h and dh go on as two parts of the activation
+ * dtype each, the rounded value and the rounded rest (they are operands of the
+ * second product); every output is rounded once. */
 
 /* Device tables of N adapters (host struct; the pointer tables hold device
  * addresses as int64 and retain nothing).  A: [rank][in], B: [rank][out] in the
@@ -307,8 +308,8 @@ size_t exl3_lora_plan_bytes(int M, int N);
 int exl3_lora_plan(const void *ids, int ids_dtype, int M, int N, void *plan, size_t plan_bytes,
                    cudaStream_t stream);
 
-/* Columns of the saved activations h for a largest rank: max_rank rounded up
- * to 16. */
+/* Columns of the saved activations h for a largest rank: twice max_rank
+ * rounded up to 16 (the values and their rests). */
 int exl3_lora_h_cols(int max_rank);
 
 /* Bytes of workspace exl3_lora_forward / exl3_lora_backward need (256-byte

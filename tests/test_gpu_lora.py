@@ -3,8 +3,8 @@
 Tolerances are elementwise bounds of the arithmetic: u = half an ulp of the
 activation type (relative); a product summed in fp32 over K terms errs by at
 most D(K) * 2^-23 * sum |terms| with D(K) = K / 16 + 32 roundings in a row (a
-chain of 16-term steps and what joins its parts); h and dh round once (u), the
-output once."""
+chain of 16-term steps and what joins its parts); h and dh are kept as a rounded
+value and the rounded rest (u^2), the output rounds once (u)."""
 import numpy as np
 import pytest
 
@@ -121,10 +121,10 @@ def check(b, forward=True, dx=True, grads=True, base=True, dx_base=True):
         xa, ga = x[on], dy[on]
         h = xa @ A.T
         eh = _acc(b.fin) * (np.abs(xa) @ np.abs(A).T)
-        eh += u * (np.abs(h) + eh) + tiny
+        eh += u * u * (np.abs(h) + eh) + tiny
         dh = s * (ga @ B.T)
         edh = _acc(b.fout) * abs(s) * (np.abs(ga) @ np.abs(B).T)
-        edh += u * (np.abs(dh) + edh) + tiny
+        edh += u * u * (np.abs(dh) + edh) + tiny
         y[on] += s * (h @ B)
         ey[on] += abs(s) * ((eh + _acc(r) * np.abs(h)) @ np.abs(B))
         dxw[on] += dh @ A

@@ -23,7 +23,7 @@ def test_router_sizes():
 
 
 def test_adapter_sizes():
-    assert [X.exl3_lora_h_cols(r) for r in (0, 1, 16, 17, 128, 129)] == [0, 16, 16, 32, 128, 0]
+    assert [X.exl3_lora_h_cols(r) for r in (0, 1, 16, 17, 128, 129)] == [0, 32, 32, 64, 256, 0]
     assert X.exl3_lora_plan_bytes(0, 1) > 0
     assert X.exl3_lora_plan_bytes(5, 0) == 0 and X.exl3_lora_plan_bytes(5, 1025) == 0
     assert X.exl3_lora_workspace_bytes(7, 2, 128, 256, 8) > 0

@@ -186,7 +186,7 @@ size_t exl3_lora_plan_bytes(int M, int N)
 
 int exl3_lora_h_cols(int max_rank)
 {
-    return max_rank >= 1 && max_rank <= EXL3_MAX_RANK ? lora_h_cols(max_rank) : 0;
+    return max_rank >= 1 && max_rank <= EXL3_MAX_RANK ? lora_h_pitch(lora_h_cols(max_rank)) : 0;
 }
 
 size_t exl3_lora_workspace_bytes(int M, int N, int in_features, int out_features, int max_rank)

@@ -45,7 +45,13 @@ EXL3_HD inline LoraPlanLayout lora_plan_layout(int M, int N)
     return L;
 }
 
+// h and dh are operands of the products that follow, and those take 16-bit
+// types.  One rounding there would be as large as the result's own (a gradient
+// that one row determines had twice the error it needs), so a row keeps h in
+// two parts, round(h) and round(h - round(h)), and a product takes both: 2
+// lora_h_cols values a row, the remainders from lora_h_cols on.
 EXL3_HD inline int lora_h_cols(int max_rank) { return (max_rank + 15) / 16 * 16; }
+EXL3_HD inline int lora_h_pitch(int h_cols) { return 2 * h_cols; }
 
 // The products share their work out evenly over at most this many CTAs (one
 // per SM); a workspace is sized for it whatever the device.
@@ -87,7 +93,7 @@ EXL3_HD inline LoraWsLayout lora_ws_layout(int M, int N, int in_f, int out_f, in
     const size_t outer = 2 * kOuterN * (size_t)kLoraCtas;
     size_t o = 0;
     L.hdr = o;  o = align_up(o + kHdrWords * 4, 256);
-    L.h = o;    o = align_up(o + (size_t)M * hc * 2, 256);
+    L.h = o;    o = align_up(o + (size_t)M * lora_h_pitch((int)hc) * 2, 256);
     L.part = o; o = align_up(o + (shrink > outer ? shrink : outer) * hc * 4, 256);
     L.total = o;
     return L;
@@ -113,7 +119,7 @@ struct LoraShrinkArgs {
     int32_t *hdr;
 };
 
-// join: h[s][j] = h_scale * (sum of shrink's partials), rounded to the activation
+// join: h[s][j] = h_scale * (sum of shrink's partials) in two parts of the activation
 // type, zero from the adapter's rank up to the next multiple of 16; h_scale:
 // the adapter's scale where `scale_h`, else 1.
 struct LoraJoinArgs {

@@ -108,6 +108,17 @@ EXL3_DEV float2 unpack2(uint32_t u, int dtype)
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
+// Two values as two parts each of the 16-bit type: hi = round(v), lo = round(v
+// - hi): 22 bits of v together for f16 (down to its smallest subnormal), 16 for
+// bf16.  Where hi overflows it stands alone, so that a product gives the
+// infinity and not inf - inf.
+EXL3_DEV void split2(float x, float y, int dtype, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack2(x, y, dtype);
+    const float2 f = unpack2(hi, dtype);
+    lo = pack2(fabsf(f.x) < INFINITY ? x - f.x : 0.0f, fabsf(f.y) < INFINITY ? y - f.y : 0.0f, dtype);
+}
+
 EXL3_DEV bool plan_ok(const int32_t *plan, int M, int N)
 {
     return plan[kLpMagic] == kLoraMagic && plan[kLpM] == M && plan[kLpN] == N && plan[kLpError] == 0;

@@ -31,22 +31,24 @@ constexpr int kMmaWarp = 16, kHWarp = 17, kHThreads = 96;
 constexpr int kTBufs = 4;           // TMEM accumulators
 constexpr int kMaxRing = 4;
 
-// Shared memory by largest rank and item width: two buffers of h, then slots
-// of 128 padded rows and a W block.
+// Shared memory by largest rank and item width: two buffers of h (one where
+// two would leave the ring two slots), then slots of 128 padded rows and a W
+// block.
 struct Geom {
-    int h_bytes, pitch, row_bytes, slot_bytes, nslots, total;
+    int h_bytes, h_bufs, pitch, row_bytes, slot_bytes, nslots, total;
 };
 template <int NW>
 EXL3_HD inline Geom geom(int h_cols)
 {
     Geom g{};
-    g.h_bytes = (h_cols + 63) / 64 * 128 * 128;
+    g.h_bytes = (2 * h_cols + 63) / 64 * 128 * 128;
+    g.h_bufs = h_cols > 96 ? 1 : 2;
     g.pitch = NW * 2 + 16;
     g.row_bytes = 128 * g.pitch;                       // a multiple of 1024
     g.slot_bytes = g.row_bytes + h_cols * NW * 2;
-    const int n = (220 * 1024 - 2 * g.h_bytes) / g.slot_bytes;
+    const int n = (220 * 1024 - g.h_bufs * g.h_bytes) / g.slot_bytes;
     g.nslots = n < kMaxRing ? n : kMaxRing;
-    g.total = 2 * g.h_bytes + g.nslots * g.slot_bytes;
+    g.total = g.h_bufs * g.h_bytes + g.nslots * g.slot_bytes;
     return g;
 }
 EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         return;
     }
     const Geom g = geom<NW>(a.h_cols);
-    uint8_t *hbuf = smem, *ring = smem + 2 * g.h_bytes;
+    uint8_t *hbuf = smem, *ring = smem + g.h_bufs * g.h_bytes;
     volatile int *abort = &c.abort;
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         }
         cp_async_wait_all();
     } else if (warp >= kHWarp) {
-        // h of each tile, K-major: rp / 8 chunks a row
+        // h of each tile, K-major: rp / 8 chunks a row, and as many of the remainders
         const int ht = tid - kHWarp * 32;
         Ring hb;
         grid_dep_wait();                           // h comes from the kernels before
@@ -196,13 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 if (!wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
                     break;
                 const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
-                const uint8_t *h = static_cast<const uint8_t *>(a.h) + (size_t)t.y * a.h_cols * 2;
-                for (int i = ht; i < t.z * hc; i += kHThreads) {
-                    const int r = i / hc, q = i % hc;
-                    cp_async16(hs + (q >> 3) * (128 * 128) + swz(r, q & 7), h + (size_t)r * a.h_cols * 2 + q * 16, true);
+                const size_t pitch = (size_t)lora_h_pitch(a.h_cols) * 2;
+                const uint8_t *h = static_cast<const uint8_t *>(a.h) + t.y * pitch;
+                for (int i = ht; i < t.z * 2 * hc; i += kHThreads) {
+                    const int r = i / (2 * hc), q = i % (2 * hc);
+                    cp_async16(hs + (q >> 3) * (128 * 128) + swz(r, q & 7),
+                               h + r * pitch + (q < hc ? q * 16 : a.h_cols * 2 + (q - hc) * 16), true);
                 }
                 cp_async_arrive(&c.hfull[hb.slot]);
-                hb.next(2);
+                hb.next(g.h_bufs);
             }
             s = (tile + 1) * nb;
         }
@@ -301,15 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 fence_proxy();
                 fence_after();
                 const uint32_t ws = smem_addr(ring + in.slot * g.slot_bytes + g.row_bytes);
-                for (int k = 0; k < rp / 16; k++)
+                const int steps = rp / 16;
+                for (int k = 0; k < 2 * steps; k++)            // h's two parts against the same W
                     mma_f16(c.tmem + t4.slot * NW, desc_k_major(hs + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                            desc_mn_major(ws + k * 2048, rp * 128), id, k > 0);
+                            desc_mn_major(ws + (k < steps ? k : k - steps) * 2048, rp * 128), id, k > 0);
                 mma_commit(&c.tfull[t4.slot]);
                 in.next(g.nslots);
                 t4.next(kTBufs);
             }
             mma_commit(&c.hempty[hb.slot]);
-            hb.next(2);
+            hb.next(g.h_bufs);
         }
         if (!ok)
             drain_mmas(&c.drain);

@@ -34,7 +34,9 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 8;       // blocks per cut item
 constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
 
-EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + (h_cols + 63) / 64 * kBlock; }
+// a stage: 64 rows of x, of h and of h's remainders
+EXL3_HD inline int part_bytes(int h_cols) { return (h_cols + 63) / 64 * kBlock; }
+EXL3_HD inline int stage_bytes(int h_cols) { return kXBytes + 2 * part_bytes(h_cols); }
 EXL3_HD inline int ring_slots(int h_cols)
 {
     const int n = kRingBytes / stage_bytes(h_cols);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             hrows = 128 / lanes;
             hr = gt / lanes;
             hn = lanes / 2;
-            h += ((size_t)(slot0 + hr) * a.h_cols + hq * 8) * 2;
+            h += ((size_t)(slot0 + hr) * lora_h_pitch(a.h_cols) + hq * 8) * 2;
             load_rows(k);
         };
         int k = begin - it.first + group;
@@ -260,13 +262,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             for (int i = 0; i < 16; i++)
                 cp_async16(dst + (ch >> 3) * kBlock + swz(r0 + 4 * i, ch & 7),
                            row[i] < 0 ? static_cast<const uint8_t *>(a.p[0].x) : x + (size_t)row[i] * pitch, row[i] >= 0);
-            const uint8_t *hk = h + (size_t)k * kOuterK * a.h_cols * 2;
+            const size_t h_pitch = (size_t)lora_h_pitch(a.h_cols) * 2;
+            const uint8_t *hk = h + k * kOuterK * h_pitch;
             if (hin)
                 for (int i = 0; i < hn; i++) {
                     const int r = hr + i * hrows;
                     const bool v = k * kOuterK + r < rows;
-                    cp_async16(dst + kXBytes + (hq >> 3) * kBlock + swz(r, hq & 7),
-                               v ? hk + (size_t)i * hrows * a.h_cols * 2 : static_cast<const uint8_t *>(a.p[0].x), v);
+                    const uint32_t to = dst + kXBytes + (hq >> 3) * kBlock + swz(r, hq & 7);
+                    const uint8_t *from = v ? hk + i * hrows * h_pitch : static_cast<const uint8_t *>(a.p[0].x);
+                    cp_async16(to, from, v);
+                    cp_async16(to + part_bytes(a.h_cols), from + (v ? a.h_cols * 2 : 0), v);
                 }
             cp_async_arrive(&c.full[put.slot]);
             put.next2(nslots);
@@ -340,9 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                 for (int half = 0; half < halves; half++)
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        mma_f16(c.tmem + (2 * t.slot + half) * kHalfCols,
-                                desc_mn_major(xs + half * 2 * kBlock + 2048 * i, kBlock),
-                                desc_mn_major(xs + kXBytes + 2048 * i, kBlock), id, !(first && i == 0));
+#pragma unroll
+                        for (int part = 0; part < 2; part++)
+                            mma_f16(c.tmem + (2 * t.slot + half) * kHalfCols,
+                                    desc_mn_major(xs + half * 2 * kBlock + 2048 * i, kBlock),
+                                    desc_mn_major(xs + kXBytes + part * part_bytes(a.h_cols) + 2048 * i, kBlock), id,
+                                    !(first && i == 0 && part == 0));
                 first = false;
                 mma_commit(&c.empty[get.slot]);
                 get.next(nslots);

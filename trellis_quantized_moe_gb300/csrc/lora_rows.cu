@@ -8,7 +8,7 @@
 // eight rows of one adapter.  Its warps share the contraction of the first
 // product in 32-wide blocks; the partial h are added warp by warp in
 // shared memory, then CTA by CTA over distributed shared memory (a fixed
-// order) and rounded once to the operand type, so every CTA has h and goes on
+// order) and split into two parts of the operand type, so every CTA has h and goes on
 // with its own columns of the second product, whose weights and base rows are
 // already on their way.
 //
@@ -76,11 +76,11 @@ EXL3_DEV uint4 ld16_or_zero(const uint8_t *p, bool in)
 }
 
 // MT: 16-rank blocks of the largest rank.  Dynamic shared memory: the warps'
-// partial h [kWarps][16 MT][8], the CTA's [16 MT][8], and h rounded [8][16 MT + 8].
+// partial h [kWarps][16 MT][8], the CTA's [16 MT][8], and h's two parts [2][8][16 MT + 8].
 template <int MT>
 constexpr int rows_smem()
 {
-    return (kWarps + 1) * 16 * MT * kRows * 4 + kRows * (16 * MT + 8) * 2;
+    return (kWarps + 1) * 16 * MT * kRows * 4 + 2 * kRows * (16 * MT + 8) * 2;
 }
 
 template <bool BF, int MT>
@@ -264,10 +264,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
         const float z[4] = {v.x * hs, v.y * hs, v.z * hs, v.w * hs};
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            const uint16_t u = (uint16_t)pack2(j < rank ? z[e] : 0.0f, 0.0f, dtype);
-            h16[(r + e) * kPitch + j] = u;
-            if (a.h && cta == 0 && r + e < t.z)
-                static_cast<uint16_t *>(a.h)[(size_t)(t.y + r + e) * a.h_cols + j] = u;
+            uint32_t hi, lo;
+            split2(j < rank ? z[e] : 0.0f, 0.0f, dtype, hi, lo);
+            h16[(r + e) * kPitch + j] = (uint16_t)hi;
+            h16[(kRows + r + e) * kPitch + j] = (uint16_t)lo;
+            if (a.h && cta == 0 && r + e < t.z) {
+                uint16_t *h = static_cast<uint16_t *>(a.h) + (size_t)(t.y + r + e) * lora_h_pitch(a.h_cols) + j;
+                h[0] = (uint16_t)hi;
+                h[a.h_cols] = (uint16_t)lo;
+            }
         }
     }
     // from here on the cluster's other CTAs may still be reading hpart
@@ -309,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
                 }
                 const uint32_t *hb = reinterpret_cast<const uint32_t *>(h16 + g * kPitch + 16 * s + 2 * q);
                 const uint32_t b0 = hb[0], b1 = hb[4];
+                const uint32_t l0 = hb[kRows * kPitch / 2], l1 = hb[kRows * kPitch / 2 + 4];
                 const uint32_t *pa = reinterpret_cast<const uint32_t *>(&f[0]);
                 const uint32_t *pb = reinterpret_cast<const uint32_t *>(&f[1]);
                 const uint32_t *pc = reinterpret_cast<const uint32_t *>(&f[2]);
@@ -319,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
                     const uint32_t a0 = prmt(pa[i / 2], pb[i / 2], sel), a1 = prmt(pa[2 + i / 2], pb[2 + i / 2], sel);
                     const uint32_t a2 = prmt(pc[i / 2], pd[i / 2], sel), a3 = prmt(pc[2 + i / 2], pd[2 + i / 2], sel);
                     mma16816<BF>(acc[i], a0, a1, a2, a3, b0, b1);
+                    mma16816<BF>(acc[i], a0, a1, a2, a3, l0, l1);
                 }
             }
         // lane: rows 2q, 2q+1 (accumulators 0, 1 of columns 0-3; 2, 3 of columns 4-7)

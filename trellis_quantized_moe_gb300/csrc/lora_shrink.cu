@@ -320,10 +320,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_join(LoraJoinArgs a)
                     v.x += f[d].x; v.y += f[d].y; v.z += f[d].z; v.w += f[d].w;
                 }
         }
-        if (err == 0)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * a.h_cols + j) = make_uint2(
-                pack2(j < rank ? v.x * alpha : 0.f, j + 1 < rank ? v.y * alpha : 0.f, a.act_dtype),
-                pack2(j + 2 < rank ? v.z * alpha : 0.f, j + 3 < rank ? v.w * alpha : 0.f, a.act_dtype));
+        if (err == 0) {
+            uint2 hi, lo;
+            split2(j < rank ? v.x * alpha : 0.f, j + 1 < rank ? v.y * alpha : 0.f, a.act_dtype, hi.x, lo.x);
+            split2(j + 2 < rank ? v.z * alpha : 0.f, j + 3 < rank ? v.w * alpha : 0.f, a.act_dtype, hi.y, lo.y);
+            uint16_t *h = static_cast<uint16_t *>(a.h) + (size_t)(t.y + r) * lora_h_pitch(a.h_cols) + j;
+            *reinterpret_cast<uint2 *>(h) = hi;
+            *reinterpret_cast<uint2 *>(h + a.h_cols) = lo;
+        }
     }
 }
 
