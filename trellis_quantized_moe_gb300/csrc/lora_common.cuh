@@ -79,6 +79,27 @@ EXL3_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
                    "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
+// 16 columns of the warp's lane quarter, to be followed by tmem_st_wait.
+EXL3_DEV void tmem_st16(uint32_t taddr, const uint4 (&v)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                     taddr),
+                 "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+                 "r"(v[1].w), "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y),
+                 "r"(v[3].z), "r"(v[3].w)
+                 : "memory");
+}
+EXL3_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// MMA whose A is in TMEM: lane = row, two consecutive k a column, 8 columns for its 16 k.
+EXL3_DEV void mma_f16_a_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+
 EXL3_DEV void tmem_alloc(uint32_t *dst, uint32_t cols)
 {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),

@@ -3,22 +3,26 @@
 // backward), with h = the sum of the shrink kernel's partials.
 //
 // Bound by reading base and writing y once (2 r products per 4 bytes).  An
-// item is a tile of 128 rows x NW outputs; a CTA takes a contiguous share of
-// the items, so a tile's h is fetched once per CTA and stays in shared memory
-// for its output blocks.  Two groups of loader warps take turns on the items
-// and copy base rows (gathered) and the W block by cp.async; an epilogue
-// thread owns a row, adds its accumulator (TMEM) to the row in place, and the
-// warp then writes its 32 rows out, 256 contiguous bytes at a time.  Row slots
-// have 16 bytes of padding: a thread per row has no bank conflicts.  (One
-// bulk copy per 256-byte row, in and out, took 38 cycles a copy: 5 us an item.)
-// NW = 128 for ranks up to 64, 64 above: the slots of a ring deep enough to
-// keep HBM busy must fit beside two 32 KB buffers of h.
+// item is a tile of 128 rows x 128 outputs; a CTA takes a contiguous share of
+// the items, so a tile's h is fetched once per CTA and stays on chip for its
+// output blocks: in TMEM, as the MMA's A, h's two parts one after the other
+// along the contraction (both against the same W block).  From shared memory
+// that doubled contraction took 53 us instead of 35 in the largest case below
+// and left the ring room for items of 64 outputs only: its rows pass through
+// shared memory four times, W's two, and A would be read anew for every item.
+// Two groups of loader warps take turns on the items and copy base rows
+// (gathered) and the W block by cp.async; an epilogue thread owns a row, adds
+// its accumulator (TMEM) to the row in place, and the warp then writes its 32
+// rows out, 128 contiguous bytes at a time.  Row slots have 16 bytes of
+// padding: a thread per row has no bank conflicts.  (One bulk copy per 256-byte
+// row, in and out, took 38 cycles a copy: 5 us an item.)
 //
 // Measured: 16384 rows, 1536 outputs, rank 16: 19.5 us for 100 MB read and
 // written (5.1 TB/s; 15.4 us at the copy rate, most of the rest before the
-// first item ends); 8192 rows, 5120 outputs, ranks 64 and 128: 38 us for
-// 168 MB, at 5.9 TB/s between the first item and the last.  Four epilogue
-// warps instead of eight took 1.9 us an item instead of 1.
+// first item ends); 8192 rows, 5120 outputs, ranks 64 and 128: 35 us after the
+// kernel before for 168 MB.  Four epilogue warps instead of eight took 1.9 us
+// an item instead of 1; a third accumulator, which fits beside h of ranks up
+// to 64, saves 0.6 us a launch (4096 rows).
 #include "lora_common.cuh"
 
 namespace exl3 {
@@ -26,41 +30,40 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 640;       // 8 loader, 8 epilogue warps, MMA warp, 3 warps for h
-constexpr int kMmaWarp = 16, kHWarp = 17, kHThreads = 96;
-constexpr int kTBufs = 4;           // TMEM accumulators
+constexpr int kThreads = 672;       // 8 loader, 8 epilogue warps, MMA warp, 4 warps for h
+constexpr int kMmaWarp = 16, kHWarp = 17, kHThreads = 128;
 constexpr int kMaxRing = 4;
+constexpr int kItemN = 128;             // outputs of an item
+constexpr int kTmemCols = 512;
+constexpr int kMaxTBufs = 3;
 
-// Shared memory by largest rank and item width: two buffers of h (one where
-// two would leave the ring two slots), then slots of 128 padded rows and a W
-// block.
+// TMEM: 3 or 2 accumulators, then two buffers of h (two parts, two values a column).
+EXL3_HD inline int h_tcols(int h_cols) { return h_cols <= 64 ? 64 : 128; }
+EXL3_HD inline int tbufs(int h_cols) { return h_cols <= 64 ? 3 : 2; }
+
+// Shared memory by largest rank: slots of 128 padded rows and a W block.
 struct Geom {
-    int h_bytes, h_bufs, pitch, row_bytes, slot_bytes, nslots, total;
+    int pitch, row_bytes, slot_bytes, nslots, total;
 };
-template <int NW>
 EXL3_HD inline Geom geom(int h_cols)
 {
     Geom g{};
-    g.h_bytes = (2 * h_cols + 63) / 64 * 128 * 128;
-    g.h_bufs = h_cols > 96 ? 1 : 2;
-    g.pitch = NW * 2 + 16;
+    g.pitch = kItemN * 2 + 16;
     g.row_bytes = 128 * g.pitch;                       // a multiple of 1024
-    g.slot_bytes = g.row_bytes + h_cols * NW * 2;
-    const int n = (220 * 1024 - g.h_bufs * g.h_bytes) / g.slot_bytes;
+    g.slot_bytes = g.row_bytes + h_cols * kItemN * 2;
+    const int n = 220 * 1024 / g.slot_bytes;
     g.nslots = n < kMaxRing ? n : kMaxRing;
-    g.total = g.h_bufs * g.h_bytes + g.nslots * g.slot_bytes;
+    g.total = g.nslots * g.slot_bytes;
     return g;
 }
-EXL3_HD inline bool narrow(int h_cols) { return h_cols > 64; }
 
 struct Ctl {
-    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kTBufs], tempty[kTBufs],
+    uint64_t hfull[2], hempty[2], full[kMaxRing], empty[kMaxRing], tfull[kMaxTBufs], tempty[kMaxTBufs],
         drain;
     uint32_t tmem;
     int abort;
 };
 
-template <int NW>
 __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     const int active = a.plan[kLpActive];
     // rows without an adapter need nothing when y is base already
     const int ntiles = a.base == a.y ? active : a.plan[kLpTiles];
-    const int nb = a.width / NW;
+    const int nb = a.width / kItemN;
     const int total = ntiles * nb, per = lora_share(total, gridDim.x, 1);
     const int begin = blockIdx.x * per, end = min(total, begin + per);
     if (begin >= end) {
@@ -93,8 +96,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             zero_fill(tid);
         return;
     }
-    const Geom g = geom<NW>(a.h_cols);
-    uint8_t *hbuf = smem, *ring = smem + g.h_bufs * g.h_bytes;
+    const Geom g = geom(a.h_cols);
+    uint8_t *ring = smem;
     volatile int *abort = &c.abort;
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             mbar_init(&c.full[i], 128);
             mbar_init(&c.empty[i], 256);
         }
-        for (int i = 0; i < kTBufs; i++) {
+        for (int i = 0; i < tbufs(a.h_cols); i++) {
             mbar_init(&c.tfull[i], 1);
             mbar_init(&c.tempty[i], 256);
         }
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         fence_mbar_init();
     }
     if (warp == kMmaWarp)
-        tmem_alloc(&c.tmem, NW * kTBufs);
+        tmem_alloc(&c.tmem, kTmemCols);
     fence_before();
     __syncthreads();
     fence_after();
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
 
     if (warp < 8) {
         // group 0 takes the even items of the share, group 1 the odd ones
-        constexpr int kLanes = NW / 8, kStep = 128 / kLanes, kN = 128 / kStep;   // lanes per row, rows a pass
+        constexpr int kLanes = kItemN / 8, kStep = 128 / kLanes, kN = 128 / kStep;   // lanes per row, rows a pass
         const int group = warp >> 2, gt = tid & 127, ch = gt % kLanes, r0 = gt / kLanes;
         Ring put;
         put.slot = group;
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             }
             if (!wait_bar(&c.empty[put.slot], put.phase ^ 1, abort, a.hdr))
                 break;
-            const size_t col = (size_t)(s - tile * nb) * (NW * 2);
+            const size_t col = (size_t)(s - tile * nb) * (kItemN * 2);
             const uint32_t dst = smem_addr(ring + put.slot * g.slot_bytes), db = dst + r0 * g.pitch + ch * 16;
             const uint8_t *base = static_cast<const uint8_t *>(a.base) + col + ch * 16;
 #pragma unroll
@@ -186,8 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         }
         cp_async_wait_all();
     } else if (warp >= kHWarp) {
-        // h of each tile, K-major: rp / 8 chunks a row, and as many of the remainders
-        const int ht = tid - kHWarp * 32;
+        // h of each tile into TMEM, a row a lane: rp / 8 chunks of 16 bytes, and
+        // as many of the rests
+        const int q = warp & 3, row = 32 * q + lane;
         Ring hb;
         grid_dep_wait();                           // h comes from the kernels before
         for (int s = begin; s < end;) {
@@ -195,25 +199,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
             const int4 t = tiles[tile];
             const int rank = tile_rank(t), hc = (rank + 15) / 16 * 2;
             if (rank > 0) {
-                if (!wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
+                if (!warp_wait_bar(&c.hempty[hb.slot], hb.phase ^ 1, abort, a.hdr))
                     break;
-                const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
-                const size_t pitch = (size_t)lora_h_pitch(a.h_cols) * 2;
-                const uint8_t *h = static_cast<const uint8_t *>(a.h) + t.y * pitch;
-                for (int i = ht; i < t.z * 2 * hc; i += kHThreads) {
-                    const int r = i / (2 * hc), q = i % (2 * hc);
-                    cp_async16(hs + (q >> 3) * (128 * 128) + swz(r, q & 7),
-                               h + r * pitch + (q < hc ? q * 16 : a.h_cols * 2 + (q - hc) * 16), true);
+                fence_after();
+                const uint32_t dst = c.tmem + ((uint32_t)(32 * q) << 16) + tbufs(a.h_cols) * kItemN + hb.slot * h_tcols(a.h_cols);
+                const uint8_t *h = static_cast<const uint8_t *>(a.h) +
+                                   (size_t)(t.y + min(row, t.z - 1)) * lora_h_pitch(a.h_cols) * 2;
+                for (int i = 0; i < 2 * hc; i += 8) {          // 2 hc is a multiple of 4
+                    uint4 v[2][4];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int k = min(i + e, 2 * hc - 1);
+                        v[e >> 2][e & 3] = *reinterpret_cast<const uint4 *>(
+                            h + (k < hc ? k * 16 : a.h_cols * 2 + (k - hc) * 16));
+                    }
+                    tmem_st16(dst + i * 4, v[0]);
+                    if (i + 4 < 2 * hc)
+                        tmem_st16(dst + i * 4 + 16, v[1]);
                 }
-                cp_async_arrive(&c.hfull[hb.slot]);
-                hb.next(g.h_bufs);
+                tmem_st_wait();
+                fence_before();
+                mbar_arrive(&c.hfull[hb.slot]);
+                hb.next(2);
             }
             s = (tile + 1) * nb;
         }
-        cp_async_wait_all();
     } else if (warp >= 8 && warp < kMmaWarp) {
         // warps 8 + q and 12 + q: rows 32 q .. 32 q + 31, half the columns each
-        constexpr int kCols = NW / 2, kLanes = kCols / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
+        constexpr int kCols = kItemN / 2, kLanes = kCols / 8, kRows = 32 / kLanes;   // rows of one warp-wide store
         const int q = warp & 3, c0 = (warp - 8) / 4 * kCols, row = 32 * q + lane;
         grid_dep_wait();                           // the error word
         const bool bad = a.hdr[kHdrError] != 0;
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 fence_after();
                 uint8_t *warp_rows = ring + in.slot * g.slot_bytes + 32 * q * g.pitch + c0 * 2;
                 uint8_t *mine = warp_rows + lane * g.pitch;
-                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * NW + c0;
+                const uint32_t acc = c.tmem + ((uint32_t)(32 * q) << 16) + t4.slot * kItemN + c0;
                 if ((mma || !a.base) && rows > 0) {            // warps past the tile's rows only keep step
 #pragma unroll
                     for (int n = 0; n < kCols; n += 32) {
@@ -260,10 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 if (mma) {
                     fence_before();
                     mbar_arrive(&c.tempty[t4.slot]);
-                    t4.next(kTBufs);
+                    t4.next(tbufs(a.h_cols));
                 }
                 __syncwarp();
-                uint8_t *out = static_cast<uint8_t *>(a.y) + (size_t)(s - tile * nb) * (NW * 2) + c0 * 2 +
+                uint8_t *out = static_cast<uint8_t *>(a.y) + (size_t)(s - tile * nb) * (kItemN * 2) + c0 * 2 +
                                lane % kLanes * 16;
 #pragma unroll
                 for (int r0 = 0; r0 < 32; r0 += kRows) {
@@ -294,10 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     in.next(g.nslots);
                 continue;
             }
-            const uint32_t id = idesc(NW, a.act_dtype, 0, 1);
+            const uint32_t id = idesc(kItemN, a.act_dtype, 0, 1);
             if (!(ok = wait_bar(&c.hfull[hb.slot], hb.phase, abort, a.hdr)))
                 break;
-            const uint32_t hs = smem_addr(hbuf + hb.slot * g.h_bytes);
+            const uint32_t hs = c.tmem + tbufs(a.h_cols) * kItemN + hb.slot * h_tcols(a.h_cols);
+            fence_after();
             for (; s < last; s++) {
                 if (!(ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr) &&
                            wait_bar(&c.tempty[t4.slot], t4.phase ^ 1, abort, a.hdr)))
@@ -307,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 const uint32_t ws = smem_addr(ring + in.slot * g.slot_bytes + g.row_bytes);
                 const int steps = rp / 16;
                 for (int k = 0; k < 2 * steps; k++)            // h's two parts against the same W
-                    mma_f16(c.tmem + t4.slot * NW, desc_k_major(hs + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                            desc_mn_major(ws + (k < steps ? k : k - steps) * 2048, rp * 128), id, k > 0);
+                    mma_f16_a_tmem(c.tmem + t4.slot * kItemN, hs + 8 * k,
+                                   desc_mn_major(ws + (k < steps ? k : k - steps) * 2048, rp * 128), id, k > 0);
                 mma_commit(&c.tfull[t4.slot]);
                 in.next(g.nslots);
-                t4.next(kTBufs);
+                t4.next(tbufs(a.h_cols));
             }
             mma_commit(&c.hempty[hb.slot]);
-            hb.next(g.h_bufs);
+            hb.next(2);
         }
         if (!ok)
             drain_mmas(&c.drain);
@@ -324,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
     fence_after();
     __syncwarp();
     if (warp == kMmaWarp)
-        tmem_free(c.tmem, NW * kTBufs);
+        tmem_free(c.tmem, kTmemCols);
 }
 
 }  // namespace
@@ -333,20 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
 
 cudaError_t lora_expand_set_attributes()
 {
-    const cudaError_t e = cudaFuncSetAttribute(lora::k_lora_expand<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               220 * 1024);
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(lora::k_lora_expand<64>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    return cudaFuncSetAttribute(lora::k_lora_expand, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
 }
 
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s)
 {
-    if (lora::narrow(a.h_cols))
-        return lora::launch_dependent(lora::k_lora_expand<64>, ctas, lora::kThreads, lora::geom<64>(a.h_cols).total,
-                                      s, a);
-    return lora::launch_dependent(lora::k_lora_expand<128>, ctas, lora::kThreads, lora::geom<128>(a.h_cols).total, s,
-                                  a);
+    return lora::launch_dependent(lora::k_lora_expand, ctas, lora::kThreads, lora::geom(a.h_cols).total, s, a);
 }
 
 }  // namespace exl3
