@@ -64,10 +64,6 @@ constexpr int kOuterN = 256;         // columns of one outer item
 // outer, 2048-row training of eight adapters 83.0 / 83.1 / 90.5 us.
 constexpr int kShrinkMin = 4;
 constexpr int kOuterMin = 4;
-// Rows up to which an outer item is never cut, so that nothing is left to
-// join: training calls with it / without it, 300 rows of one adapter 21 / 24.6
-// us, 1100 rows of four 54.9 / 57.4, but 1500 rows of two 54.4 / 50.5.
-constexpr int kOuterWholeRows = 512;
 
 // `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).
 EXL3_HD inline int lora_share(int total, int ctas, int least)
@@ -167,7 +163,6 @@ struct LoraRowsArgs {
 struct LoraOuterArgs {
     const int32_t *plan;
     int M, N, act_dtype, h_cols, ctas;
-    int whole;                      // shares end at items' ends: no partials, no join kernel
     const int32_t *rank;
     const float *scale;
     struct Product {
@@ -185,7 +180,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkArgs &a, int ctas, cudaStream_t s
 cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraExpandArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_lora_rows(LoraRowsArgs a, int sms, cudaStream_t s);
-cudaError_t launch_lora_outer(LoraOuterArgs a, cudaStream_t s);
+cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s);
 cudaError_t lora_plan_set_attributes();
 cudaError_t lora_shrink_set_attributes();
 cudaError_t lora_expand_set_attributes();

@@ -24,7 +24,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 480;       // 8 loader warps in two groups, 4 epilogue, MMA, fence, zero warp
+constexpr int kThreads = 448;       // 8 loader warps in two groups, 4 epilogue, MMA, fence warp
 constexpr int kBlock = 64 * 128;                 // 64 rows of 64 columns
 constexpr int kXBytes = kOuterN / 64 * kBlock;
 constexpr int kHalfCols = 128;                   // TMEM columns of one 128-column half
@@ -114,15 +114,15 @@ EXL3_DEV void store16(void *p, size_t i, int dtype, float v)
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// Zero gradients for the adapters without rows, dealt to `of` workers of n threads.
-EXL3_DEV void zero_unused(const LoraOuterArgs &a, const int32_t *steps, int worker, int of, int i0, int n)
+// Zero gradients for the adapters without rows, dealt to `of` CTAs of the join.
+EXL3_DEV void zero_unused(const LoraOuterArgs &a, const int32_t *steps, int worker, int of)
 {
     for (int e = worker; e < a.N; e += of) {
         if (steps[e] != steps[e + 1] || a.rank[e] == 0)
             continue;
         for (int p = 0; p < 2; p++) {
             uint4 *out = reinterpret_cast<uint4 *>(a.p[p].G[e]);
-            for (size_t i = i0; i < (size_t)a.rank[e] * a.p[p].width / 8; i += n)
+            for (size_t i = threadIdx.x; i < (size_t)a.rank[e] * a.p[p].width / 8; i += kJoinThreads)
                 out[i] = make_uint4(0, 0, 0, 0);
         }
     }
@@ -133,7 +133,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Ctl c;
     __shared__ Item start;
-    __shared__ int share[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_launch();
     // (a CTA that has nothing to do waits too: the join takes this kernel's end
@@ -145,27 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
     const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kOuterMin);
-    int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
-    if (a.whole) {
-        // the items that start in the share
-        if (warp < 2) {
-            int s = warp ? end : begin;
-            if (s < total) {
-                const Item it = locate(a, steps, s);
-                s = it.first == s ? s : it.first + it.len;
-            }
-            if (lane == 0)
-                share[warp] = s;
-        }
-        if (warp == 14) {
-            grid_dep_wait();
-            if (a.hdr[kHdrError] == 0)
-                zero_unused(a, steps, blockIdx.x, gridDim.x, lane, 32);
-        }
-        __syncthreads();
-        begin = share[0];
-        end = share[1];
-    }
+    const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
     if (begin >= end) {
         grid_dep_wait();
         return;
@@ -400,7 +379,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
         grid_dep_wait();
         if (a.hdr[kHdrError])
             return;
-        zero_unused(a, steps, blockIdx.x - a.ctas * kJoinParts, kZeroBlocks, threadIdx.x, kJoinThreads);
+        zero_unused(a, steps, blockIdx.x - a.ctas * kJoinParts, kZeroBlocks);
         return;
     }
     const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kOuterMin);
@@ -464,14 +443,13 @@ cudaError_t lora_outer_set_attributes()
                                 lora::kRingBytes);
 }
 
-cudaError_t launch_lora_outer(LoraOuterArgs a, cudaStream_t s)
+cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s)
 {
-    a.whole = a.M > 0 && a.M <= kOuterWholeRows;
     if (a.M > 0) {
         const cudaError_t e =
             lora::launch_dependent(lora::k_lora_outer, a.ctas, lora::kThreads,
                                    lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s, a);
-        if (e != cudaSuccess || a.whole)
+        if (e != cudaSuccess)
             return e;
     }
     return lora::launch_dependent(lora::k_lora_outer_join, a.ctas * lora::kJoinParts + lora::kZeroBlocks,
