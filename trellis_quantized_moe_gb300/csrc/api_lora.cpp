@@ -52,11 +52,13 @@ int product_ctas(int sms) { return sms < kLoraCtas ? sms : kLoraCtas; }
 // Rows up to which one launch does both products.  It reads a weight once per
 // eight rows (from L2), the products' own kernels once per 128, at the price of
 // two launches and partial sums between them.  GPU time of a call, one launch /
-// two (bf16, us): 5120 -> 1536, rank 16: 1 row 4.6 / 10.6, 512 rows 6.6 / 15.0,
-// 1024 rows 8.7 / 15.6, 1500 rows 14.1 / 16.4, 2048 rows 16.1 / 17.3, 4096 rows
-// 31.5 / 20.3; rank 64: 1024 rows 17.7 / 19.9, 1500 rows 28.4 / 20.8; 1536 ->
-// 5120: rank 16, 1024 rows 11.3 / 15.6, 1500 rows 20.1 / 15.9.
-constexpr int kRowsMax = 1024;
+// two (bf16, us): 5120 -> 1536, rank 16: 1 row 4.3 / 10.8, 512 rows 7.2 / 13.8,
+// 1024 rows 10.8 / 16.7, 1500 rows 17.5 / 17.7, 2048 rows 19.6 / 19.5, 4096 rows
+// 37.6 / 25.3; rank 64: 1024 rows 19.7 / 20.7, 1500 rows 33.1 / 21.6; 1536 ->
+// 5120: rank 16, 1024 rows 13.3 / 17.7, 1500 rows 23.2 / 19.0.  Its registers hold
+// less of a wide adapter: 2048 -> 2048, rank 128: 512 rows 17.9 / 19.6, 1024 rows
+// 26.0 / 21.1.
+int rows_max(int max_rank) { return max_rank <= 64 ? 1024 : 512; }
 
 // h = h_scale * W1 x, y = base + y_scale * h W2 of a batch (scale_h: the
 // adapter's scale goes to h instead of y), and the check of the tables.
@@ -248,7 +250,7 @@ int exl3_lora_forward(const void *x, int act_dtype, int M, const exl3_adapters *
                      h ? h : static_cast<uint8_t *>(ws) + L.h};
     const int ctas = product_ctas(sms);
     cudaError_t e;
-    if (M <= kRowsMax) {
+    if (M <= rows_max(ad->max_rank)) {
         e = launch_lora_rows(rows_args(p, act_dtype, M, ad, nullptr, plan, ws), sms, stream);
     } else {
         e = run_shrink(p, act_dtype, M, ad, nullptr, plan, ws, L, ctas, stream);
@@ -298,7 +300,7 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
         o.p[1] = {dy, h, grads->B, ad->out_features, 1};
     }
     cudaError_t e;
-    if (M <= kRowsMax) {
+    if (M <= rows_max(ad->max_rank)) {
         e = launch_lora_rows(rows_args(p, act_dtype, M, ad, grads, plan, ws), sms, stream);
         if (e == cudaSuccess && grads)
             e = launch_lora_outer(o, stream);

@@ -21,6 +21,7 @@ enum LoraPlanWord {
     kLpSmallTiles = 5,
     kLpActive = 6,     // prompt tiles of adapters
     kLpSmallActive = 7,
+    kLpUsed = 8,       // adapters that have rows
     kLpWords = 64
 };
 
@@ -60,10 +61,19 @@ constexpr int kShrinkK = 128;        // inputs of one shrink stage
 constexpr int kOuterK = 64;          // rows of one outer stage
 constexpr int kOuterN = 256;         // columns of one outer item
 // Stages below which a CTA is not worth its share.  With 2 / 4 / 8: shrink,
-// 1100-row forward 15.5 / 15.3 / 16.6 us, 4096-row training 73.2 / 72.4 / 73.9;
-// outer, 2048-row training of eight adapters 83.0 / 83.1 / 90.5 us.
+// 1100-row forward 17.1 / 16.5 / 17.7 us, 4096-row training 75.9 / 74.9 / 76.1.
+// An outer share is no shorter than a mean item (its stages: steps of the
+// adapters that have rows) up to kOuterMin, so that short items are spread out
+// and few are cut.  Training with least shares of 1 / 2 / 4 stages: 8 rows, rank
+// 8, 13.3 / 14.2 / 16.6 us; 300 rows of four adapters of rank 16, 22.2 / 18.3 /
+// 19.9; 256 rows of one of rank 128, 45.7 / 43.5 / 36.0.
 constexpr int kShrinkMin = 4;
 constexpr int kOuterMin = 4;
+EXL3_HD inline int lora_outer_min(int steps, int used)
+{
+    const int mean = steps / (used > 1 ? used : 1);
+    return mean < 1 ? 1 : mean < kOuterMin ? mean : kOuterMin;
+}
 
 // `total` units in contiguous shares: CTA c takes [c*per, (c+1)*per).
 EXL3_HD inline int lora_share(int total, int ctas, int least)

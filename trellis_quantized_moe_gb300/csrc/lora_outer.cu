@@ -106,14 +106,6 @@ EXL3_DEV int total_stages(const LoraOuterArgs &a, const int32_t *steps)
     return steps[a.N] * (blocks(a.p[0].width) + blocks(a.p[1].width));
 }
 
-EXL3_DEV void store16(void *p, size_t i, int dtype, float v)
-{
-    if (dtype == EXL3_BF16)
-        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
-
 // Zero gradients for the adapters without rows, dealt to `of` CTAs of the join.
 EXL3_DEV void zero_unused(const LoraOuterArgs &a, const int32_t *steps, int worker, int of)
 {
@@ -143,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     }
     const LoraPlanLayout L = lora_plan_layout(a.M, a.N);
     const int32_t *perm = a.plan + L.perm / 4, *steps = a.plan + L.steps / 4, *offs = a.plan + L.offsets / 4;
-    const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, kOuterMin);
+    const int least = lora_outer_min(steps[a.N], a.plan[kLpUsed]);
+    const int total = total_stages(a, steps), per = lora_share(total, gridDim.x, least);
     const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
     if (begin >= end) {
         grid_dep_wait();
@@ -273,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             const bool whole = it.first >= begin && it.first + it.len <= end;
             const int rank = bad ? 0 : a.rank[it.e], width = a.p[it.p].width;
             const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
-            void *out = rank > 0 ? reinterpret_cast<void *>(a.p[it.p].G[it.e]) : nullptr;
+            uint16_t *out = rank > 0 ? reinterpret_cast<uint16_t *>(a.p[it.p].G[it.e]) + it.n * kOuterN + col : nullptr;
             float *part = a.part + (2 * (size_t)blockIdx.x + (s > begin)) * kOuterN * a.h_cols + col;
             if (!warp_wait_bar(&c.tfull[t.slot], t.phase, abort, a.hdr))
                 break;
@@ -286,11 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                     tmem_ld16_issue(addr + j, v);
                     tmem_ld16_wait(v);
                     if (whole) {
+                        uint16_t *o = out + (size_t)j * width + half * 128;
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
+                        for (int i = 0; i < 16; i += 2, o += 2 * width) {
+                            const uint32_t u = pack2(alpha * __uint_as_float(v[i]), alpha * __uint_as_float(v[i + 1]),
+                                                     a.act_dtype);
                             if (j + i < rank)
-                                store16(out, (size_t)(j + i) * width + it.n * kOuterN + half * 128 + col,
-                                        a.act_dtype, alpha * __uint_as_float(v[i]));
+                                o[0] = (uint16_t)u;
+                            if (j + i + 1 < rank)
+                                o[width] = (uint16_t)(u >> 16);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; i++)
@@ -382,7 +380,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
         zero_unused(a, steps, blockIdx.x - a.ctas * kJoinParts, kZeroBlocks);
         return;
     }
-    const int total = total_stages(a, steps), per = lora_share(total, a.ctas, kOuterMin);
+    const int least = lora_outer_min(steps[a.N], a.plan[kLpUsed]);
+    const int total = total_stages(a, steps), per = lora_share(total, a.ctas, least);
     const int cut = (share + 1) * per;
     if (cut >= total)
         return;

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_plan(LoraPlanArgs a)
         offsets[N] = total;
         offsets[N + 1] = M;
     }
-    __syncthreads();
+    const int used = __syncthreads_count(tid < N && rows > 0);
     for (int i = 0; i < steps; i++) {
         const int r = r0 + i * 32 + lane;
         const int g = r < M ? group(r) : -1;
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_plan(LoraPlanArgs a)
         a.plan[kLpM] = M;
         a.plan[kLpN] = N;
         a.plan[kLpActive] = ntiles;
+        a.plan[kLpUsed] = used;
         a.plan[kLpSmallActive] = nsmall;
         a.plan[kLpTiles] = ntiles + (idle + kLoraTile - 1) / kLoraTile;
         a.plan[kLpSmallTiles] = nsmall + (idle + kLoraSmallTile - 1) / kLoraSmallTile;
