@@ -13,10 +13,14 @@
 // MN-major (x^T gives the 128 accumulator lanes, h the columns), so nothing is
 // transposed.
 //
-// Measured: 8192 rows, 5120 and 1536 columns, ranks 64 and 128: 29 us for 109 MB,
-// 0.85 us a stage (5.7 TB/s of x and dy, as much again of h from L2), then 8.6
-// us to join 40 MB of partials.  300 rows, 4096 and 1408 columns, rank 8, items
-// uncut: 7 us after the kernel before (cut, with the join: 9).
+// h comes in two parts (its rounded value and the rest), each a B operand of
+// its own beside the same x: an MMA costs more when its x changes, so the two
+// follow each other (alternating between the halves of x instead: 81 us for 77,
+// 4096-row training of rank 32; one MMA of both parts' columns is no faster).
+//
+// Measured: 8192 rows, 5120 and 1536 columns, ranks 64 and 128: 31 us after the
+// kernel before for 109 MB, then 9 us to join 40 MB of partials.  300 rows, 4096
+// and 1408 columns, rank 8: 6 and 2 us.
 #include "lora_common.cuh"
 
 namespace exl3 {
@@ -31,7 +35,7 @@ constexpr int kHalfCols = 128;                   // TMEM columns of one 128-colu
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxSlots = 6;
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 8;       // blocks per cut item
+constexpr int kJoinParts = 4;       // blocks per boundary that cuts an item
 constexpr int kZeroBlocks = 64;     // join kernel: blocks that zero unused adapters' gradients
 
 // a stage: 64 rows of x, of h and of h's remainders
@@ -360,9 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         tmem_free(c.tmem, 4 * kHalfCols);
 }
 
-// Blocks 8c .. 8c + 7, c < ctas: an eighth each of the item that the boundary
-// between shares c and c + 1 cuts, if c holds the item's first stage.  The
-// other blocks zero the gradients of adapters without rows.
+// Blocks 4c .. 4c + 3, c < ctas, work on the item that the boundary between
+// shares c and c + 1 cuts, if it cuts one: an item has four blocks for each
+// boundary in it, so that one with many partials is spread out too (7518 rows
+// of one adapter of rank 68, 17 partials an item: 10 us; with eight blocks an
+// item, whatever its partials, 15).  The other blocks zero the gradients of
+// adapters without rows.
 __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs a)
 {
     grid_dep_launch();
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
         return;
     const Item it = locate(a, steps, cut);
     const int c0 = it.first / per, c1 = (it.first + it.len - 1) / per;
-    if (it.first == cut || c0 != share)
+    if (it.first == cut)
         return;
     const int rank = a.rank[it.e], width = a.p[it.p].width;
     const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
@@ -398,8 +405,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
         return;
     uint8_t *out = reinterpret_cast<uint8_t *>(a.p[it.p].G[it.e]);
     // four columns a thread
-    constexpr int kU = 4, kStep = kJoinParts * kJoinThreads, kC = 2;   // kU * kC loads in flight
-    for (int i0 = (blockIdx.x % kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * quads; i0 += kU * kStep) {
+    constexpr int kU = 4, kC = 2;                  // kU * kC loads in flight
+    const int step = (c1 - c0) * kJoinParts * kJoinThreads;
+    for (int i0 = (blockIdx.x - c0 * kJoinParts) * kJoinThreads + threadIdx.x; i0 < rank * quads; i0 += kU * step) {
         float4 v[kU] = {};
         for (int c = c0; c <= c1; c += kC) {
             float4 f[kC][kU];
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
                 const float *p = a.part + (2 * (size_t)(c + d) + (max(it.first, (c + d) * per) > (c + d) * per)) * slot;
 #pragma unroll
                 for (int u = 0; u < kU; u++) {
-                    const int i = i0 + u * kStep;
+                    const int i = i0 + u * step;
                     f[d][u] = c + d <= c1 && i < rank * quads
                                   ? *reinterpret_cast<const float4 *>(p + i / quads * kOuterN + i % quads * 4)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
         }
 #pragma unroll
         for (int u = 0; u < kU; u++) {
-            const int i = i0 + u * kStep;
+            const int i = i0 + u * step;
             if (i < rank * quads)
                 *reinterpret_cast<uint2 *>(out + ((size_t)(i / quads) * width + it.n * kOuterN + i % quads * 4) * 2) =
                     make_uint2(pack2(alpha * v[u].x, alpha * v[u].y, a.act_dtype),
