@@ -540,3 +540,19 @@ def test_refuses_host_memory_and_short_buffers():
     assert e.value.code == -6
     torch.cuda.synchronize()
     assert torch.isnan(b.y).all()
+
+
+def test_an_overflowing_h_is_an_infinity():
+    """f16, h beyond 65504: infinities of the product's sign, not NaN, and no other row is touched."""
+    b = Batch([0, 0, 1], [16, 16], 256, 128, "f16")
+    b.A[0].fill_(4.0)
+    b.B[0].fill_(1.0)
+    b.x[0].fill_(100.0)             # h = 102400 in every rank
+    b.x[1].fill_(0.5)
+    b.make_plan()
+    b.forward()
+    torch.cuda.synchronize()
+    assert bool((b.y[0] == float("inf")).all())
+    want = _f64(b.base[1]) + 2.0 * 16 * 512
+    assert np.all(np.abs(_f64(b.y[1]) - want) <= 2.0 ** -11 * np.abs(want) * 1.01)
+    assert bool(torch.isfinite(b.y[2:]).all())

@@ -8,9 +8,9 @@
 // eight rows of one adapter.  Its warps share the contraction of the first
 // product in 32-wide blocks; the partial h are added warp by warp in
 // shared memory, then CTA by CTA over distributed shared memory (a fixed
-// order) and split into two parts of the operand type, so every CTA has h and goes on
-// with its own columns of the second product, whose weights and base rows are
-// already on their way.
+// order) and split into two parts of the operand type, so every CTA has h and
+// goes on with its own columns of the second product, whose weights and base
+// rows are already on their way.
 //
 // Operands go from global memory to mma.sync fragments directly, 16 bytes a
 // lane.  First product (M = ranks, N = rows): a lane's eight consecutive k
@@ -20,11 +20,14 @@
 // interleaves pairs; MMA i takes columns 8g+i and 8g+i+4 as its rows g and
 // g+8, so that a lane ends up with eight consecutive columns of two rows of y.
 //
-// Measured (bf16, 5120 -> 1536): one row, rank 16: 4.2 us; 64 rows over 40
-// adapters of ranks 8 to 64: 8.7 us for 20 MB (2.3 TB/s).  What it spends: 2 us
+// The second product takes h's two parts (its rounded value and the rest) as
+// B operands beside the same weights: 0.5 us of the 64 rows below.
+//
+// Measured (bf16, 5120 -> 1536): one row, rank 16: 4.7 us; 64 rows over 40
+// adapters of ranks 8 to 64: 10.7 us for 20 MB (1.9 TB/s).  What it spends: 2 us
 // on plan and tables, 4 on the first product's weights (three rounds of loads
 // of what the registers hold), 1 each on the two reductions and the second
-// product.  Sixteen-row tiles, three CTAs an SM and deeper or shallower rounds
+// product, the rest on start and end.  Sixteen-row tiles, three CTAs an SM and deeper or shallower rounds
 // were no faster.
 #include "lora_common.cuh"
 

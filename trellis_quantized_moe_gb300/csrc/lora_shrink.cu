@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_shrink(LoraShrinkArgs a)
         tmem_free(c.tmem, 2 * kBufCols);
 }
 
-// Adds a tile's partials and rounds them once to the second product's operand.
+// Adds a tile's partials and splits the sums into the second product's operands.
 // A thread has four columns of one row and the partials of four CTAs in flight
 // (they lie in L2); a block takes as many rows as its threads have at the
 // largest rank.

@@ -14,9 +14,9 @@
 // w_i (d_i - sum_j w_j d_j) at the chosen experts.
 //
 // What bounds it: not HBM but the instructions per row, most of them the
-// choice's.  Measured at 65536 x 192 bf16, top 8: forward with the balance 30 us
-// (371 instructions a row, the ALU pipe 68% busy, DRAM 9%), join 5 us, backward
-// 22 us (293 instructions a row).
+// choice's.  Measured at 65536 x 192 bf16, top 8: forward with the balance 29 us
+// (346 instructions a row, 75% of the issue slots, the ALU pipe 58% busy, DRAM
+// 11%), join 5 us, backward 21 us (232 instructions a row).
 #include <type_traits>
 
 #include "common.cuh"
