@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         }
         for (int i = 0; i < kMaxRing; i++) {
             mbar_init(&c.full[i], 128);
-            mbar_init(&c.empty[i], 256);
+            mbar_init(&c.empty[i], 257);             // the epilogue's threads and the MMA thread
         }
         for (int i = 0; i < tbufs(a.h_cols); i++) {
             mbar_init(&c.tfull[i], 1);
@@ -302,9 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
         for (int s = begin; s < end && ok;) {
             const int tile = s / nb, last = min(end, (tile + 1) * nb);
             const int rank = tile_rank(tiles[tile]), rp = (rank + 15) / 16 * 16;
+            // Items without an MMA (no adapter, or one of rank 0) are waited for
+            // and handed back all the same: a thread that left them out could be
+            // a whole turn of the ring ahead of the loaders, or behind them, and
+            // the phase's parity would not tell.
             if (rank == 0) {
-                for (; s < last; s++)
+                for (; s < last; s++) {
+                    if (!(ok = wait_bar(&c.full[in.slot], in.phase, abort, a.hdr)))
+                        break;
+                    mbar_arrive(&c.empty[in.slot]);
                     in.next(g.nslots);
+                }
                 continue;
             }
             const uint32_t id = idesc(kItemN, a.act_dtype, 0, 1);
@@ -324,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                     mma_f16_a_tmem(c.tmem + t4.slot * kItemN, hs + 8 * k,
                                    desc_mn_major(ws + (k < steps ? k : k - steps) * 2048, rp * 128), id, k > 0);
                 mma_commit(&c.tfull[t4.slot]);
+                mbar_arrive(&c.empty[in.slot]);        // (the epilogue's wait for the MMAs' end)
                 in.next(g.nslots);
                 t4.next(tbufs(a.h_cols));
             }
