@@ -280,8 +280,10 @@ int exl3_router_backward(const void *logits, int logits_dtype, int M, int E, int
  *   dA_a = sum_t dh_t x_t^T,  dB_a = scale_a * sum_t h_t dy_t^T.
  * Products accumulate in fp32; h and dh go on as two parts of the activation
  * dtype each, the rounded value and the rounded rest (they are operands of the
- * second product); every output is rounded once.  With f16, h or dh beyond
- * 65504 is an infinity. */
+ * second product): together 16 bits of a bf16 value, 22 bits of an f16 one (the
+ * rest is kept times 2^11; below 2^-14 the error is at most 2^-36).  Every
+ * output is rounded once.  With f16, h or dh beyond 65504 is an infinity.  Where
+ * an operand is infinite, an output it enters is an infinity or a NaN. */
 
 /* Device tables of N adapters (host struct; the pointer tables hold device
  * addresses as int64 and retain nothing).  A: [rank][in], B: [rank][out] in the

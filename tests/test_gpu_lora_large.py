@@ -132,3 +132,38 @@ def test_rank_zero_between_short_runs():
     groups = [(e, 128 * (1 + e % 3) - (e % 2) * 40) for e in range(30)]
     b = Large(groups, [0 if e % 2 == 0 else 16 for e in range(30)], 256, 1024, "bf16", seed=3).run()
     check(b)
+
+
+# f16 with small h or dh, as at the start of a fine-tuning (B near zero), with
+# small gradients or with small activations.  The two parts of h and dh hold 22
+# bits down to 2^-14 and 2^-36 absolute below; with an absolute error of 2^-25 these
+# gradients are 0.1 to 0.3% off.  Bound, of the Frobenius norm: one
+# rounding of every element (u, or half the subnormal spacing), 2^-15 for sums
+# of up to 4096 terms in fp32 (random signs: sqrt(4096) roundings of 2^-24 and
+# the partial sums' are 2^-18; 8 times that), and 2^-36 in every h and dh.
+_SMALL = [dict(B=1e-5, dy=2e-2, A=1000.0), dict(B=1e-4, dy=1e-3, A=1000.0), dict(x=1e-3, A=1e-2, B=50.0)]
+
+
+def check_norms(b):
+    u, tiny, floor = 2.0 ** -11, 2.0 ** -25, 2.0 ** -36
+    for a in range(b.N):
+        on = torch.nonzero(b.ids == a).squeeze(1)
+        A, B, s, x, dy = b.A[a].double(), b.B[a].double(), b.scales[a], b.x[on].double(), b.dy[on].double()
+        h, dh = x @ A.T, s * (dy @ B.T)
+        one = torch.ones_like(h)
+        for got, want, spread, what in ((b.y[on], s * (h @ B), one @ B.square(), "y"),
+                                        (b.dx[on], dh @ A, one @ A.square(), "dx"),
+                                        (b.dA[a], dh.T @ x, one.T @ x.square(), "dA"),
+                                        (b.dB[a], s * (h.T @ dy), s * s * (one.T @ dy.square()), "dB")):
+            rounding = torch.clamp(u * want.abs(), min=tiny)
+            bound = float(rounding.norm() + 2.0 ** -15 * want.norm() + floor * spread.sqrt().norm())
+            off = float((got.double() - want).norm())
+            assert off <= bound, f"{what} of {a}: {off / float(want.norm()):.2e}, {bound / float(want.norm()):.2e} allowed"
+
+
+@pytest.mark.parametrize("sizes", _SMALL, ids=["small B", "small dy", "small x"])
+@pytest.mark.parametrize("groups,ranks,fin,fout", [
+    ([(0, 300)], [8], 4096, 1408), ([(0, 150), (1, 250)], [100, 30], 1536, 1024),
+    ([(0, 2000), (1, 1100)], [8, 40], 1536, 2048), ([(1, 1300), (0, 1000)], [128, 70], 2048, 1024)])
+def test_small_values_keep_their_bits(groups, ranks, fin, fout, sizes):
+    check_norms(Large(groups, ranks, fin, fout, "f16", seed=len(ranks), **sizes).run("null"))

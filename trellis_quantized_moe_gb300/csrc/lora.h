@@ -49,8 +49,8 @@ EXL3_HD inline LoraPlanLayout lora_plan_layout(int M, int N)
 // h and dh are operands of the products that follow, and those take 16-bit
 // types.  One rounding there would be as large as the result's own (a gradient
 // that one row determines had twice the error it needs), so a row keeps h in
-// two parts, round(h) and round(h - round(h)), and a product takes both: 2
-// lora_h_cols values a row, the remainders from lora_h_cols on.
+// two parts, round(h) and the rounded rest (split2 in lora_common.cuh), and a
+// product takes both: 2 lora_h_cols values a row, the rests from lora_h_cols on.
 EXL3_HD inline int lora_h_cols(int max_rank) { return (max_rank + 15) / 16 * 16; }
 EXL3_HD inline int lora_h_pitch(int h_cols) { return 2 * h_cols; }
 

@@ -328,9 +328,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_expand(LoraExpandArgs a)
                 fence_after();
                 const uint32_t ws = smem_addr(ring + in.slot * g.slot_bytes + g.row_bytes);
                 const int steps = rp / 16;
-                for (int k = 0; k < 2 * steps; k++)            // h's two parts against the same W
-                    mma_f16_a_tmem(c.tmem + t4.slot * kItemN, hs + 8 * k,
-                                   desc_mn_major(ws + (k < steps ? k : k - steps) * 2048, rp * 128), id, k > 0);
+                // h's two parts against the same W: the rests first, whose sum
+                // the first MMA of the values then divides
+                const uint32_t acc = c.tmem + t4.slot * kItemN, rests = hs + 8 * steps;
+                for (int k = 0; k < steps; k++)
+                    mma_f16_a_tmem(acc, rests + 8 * k, desc_mn_major(ws + k * 2048, rp * 128), id, k > 0);
+                if (a.act_dtype == EXL3_F16)
+                    mma_f16_a_tmem_unscale(acc, hs, desc_mn_major(ws, rp * 128), id);
+                else
+                    mma_f16_a_tmem(acc, hs, desc_mn_major(ws, rp * 128), id, true);
+                for (int k = 1; k < steps; k++)
+                    mma_f16_a_tmem(acc, hs + 8 * k, desc_mn_major(ws + k * 2048, rp * 128), id, true);
                 mma_commit(&c.tfull[t4.slot]);
                 mbar_arrive(&c.empty[in.slot]);        // (the epilogue's wait for the MMAs' end)
                 in.next(g.nslots);

@@ -47,6 +47,15 @@ EXL3_HD inline int ring_slots(int h_cols)
     return n < kMaxSlots ? n : kMaxSlots;
 }
 
+// TMEM: two accumulators of two halves, one filled while the other is drained.
+// f16 sums the rests of h apart (split2), in the columns that ranks up to 64
+// leave free; above, in the other accumulator's, so that there is only one (f16,
+// 8192 rows, training, against bf16 or the rests in the same columns: ranks 64 and
+// 128, 141 us and 140; 40 adapters of rank 100, whose items have four stages, 172
+// and 153).
+EXL3_HD inline int tbufs(int h_cols, int dtype) { return dtype == EXL3_F16 && h_cols > 64 ? 1 : 2; }
+EXL3_HD inline int rest_cols(int h_cols, int dtype) { return dtype != EXL3_F16 ? 0 : h_cols <= 64 ? 64 : 2 * kHalfCols; }
+
 struct Ctl {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2], drain;
     uint32_t tmem;
@@ -265,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
         Ring t;
         grid_dep_wait();            // and so does the error word
         const bool bad = a.hdr[kHdrError] != 0;
+        const int nbufs = tbufs(a.h_cols, a.act_dtype), rests = rest_cols(a.h_cols, a.act_dtype);
         for (int s = begin; s < end;) {
             const int stop = min(end, it.first + it.len);
             const bool whole = it.first >= begin && it.first + it.len <= end;
@@ -282,6 +292,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                     uint32_t v[16];
                     tmem_ld16_issue(addr + j, v);
                     tmem_ld16_wait(v);
+                    if (rests) {
+                        uint32_t w[16];
+                        tmem_ld16_issue(addr + rests + j, w);
+                        tmem_ld16_wait(w);
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), 1.0f / (1 << kRestBits), __uint_as_float(v[i])));
+                    }
                     if (whole) {
                         uint16_t *o = out + (size_t)j * width + half * 128;
 #pragma unroll
@@ -302,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
             }
             fence_before();
             mbar_arrive(&c.tempty[t.slot]);
-            t.next(2);
+            t.next(nbufs);
             s = stop;
             if (s < end)
                 next_item(a, steps, it);
@@ -310,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
     } else if (warp == 12 && lane == 0) {
         Ring get, t;
         bool ok = true;
+        const int nbufs = tbufs(a.h_cols, a.act_dtype), rests = rest_cols(a.h_cols, a.act_dtype);
         for (int s = begin; s < end && ok;) {
             const int stop = min(end, it.first + it.len);
             const uint32_t id = idesc(padded_rank(it.e), a.act_dtype, 1, 1);
@@ -328,16 +347,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
                     for (int i = 0; i < 4; i++)
 #pragma unroll
                         for (int part = 0; part < 2; part++)
-                            mma_f16(c.tmem + (2 * t.slot + half) * kHalfCols,
+                            mma_f16(c.tmem + (2 * t.slot + half) * kHalfCols + part * rests,
                                     desc_mn_major(xs + half * 2 * kBlock + 2048 * i, kBlock),
                                     desc_mn_major(xs + kXBytes + part * part_bytes(a.h_cols) + 2048 * i, kBlock), id,
-                                    !(first && i == 0 && part == 0));
+                                    !(first && i == 0 && (part == 0 || rests)));
                 first = false;
                 mma_commit(&c.empty[get.slot]);
                 get.next(nslots);
             }
             mma_commit(&c.tfull[t.slot]);
-            t.next(2);
+            t.next(nbufs);
             if (s < end)
                 next_item(a, steps, it);
         }

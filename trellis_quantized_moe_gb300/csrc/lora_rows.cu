@@ -283,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
     __syncthreads();
     const float ys = a.scale_h ? 1.0f : alpha;
     for (int grp = first; grp < groups; grp += all_warps) {
-        float acc[4][4];
+        constexpr int kAcc = BF ? 4 : 8, kRest = kAcc - 4;     // f16: the rests' products from kRest on
+        float acc[kAcc][4];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < kAcc; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 acc[i][e] = 0.0f;
@@ -328,9 +329,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows(LoraRowsArgs a)
                     const uint32_t a0 = prmt(pa[i / 2], pb[i / 2], sel), a1 = prmt(pa[2 + i / 2], pb[2 + i / 2], sel);
                     const uint32_t a2 = prmt(pc[i / 2], pd[i / 2], sel), a3 = prmt(pc[2 + i / 2], pd[2 + i / 2], sel);
                     mma16816<BF>(acc[i], a0, a1, a2, a3, b0, b1);
-                    mma16816<BF>(acc[i], a0, a1, a2, a3, l0, l1);
+                    mma16816<BF>(acc[kRest + i], a0, a1, a2, a3, l0, l1);
                 }
             }
+        if constexpr (!BF) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    acc[i][e] = fmaf(acc[kRest + i][e], 1.0f / (1 << kRestBits), acc[i][e]);
+        }
         // lane: rows 2q, 2q+1 (accumulators 0, 1 of columns 0-3; 2, 3 of columns 4-7)
 #pragma unroll
         for (int i = 0; i < 2; i++) {
