@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_outer(LoraOuterArgs a)
 __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs a)
 {
     grid_dep_launch();
+    // (a CTA that has nothing to do waits too: the kernel after this one takes
+    // its end for the end of the kernels before)
     if (!plan_ok(a.plan, a.M, a.N)) {
         grid_dep_wait();
         return;
@@ -409,12 +411,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_lora_outer_join(LoraOuterArgs 
     const int least = lora_outer_min(steps[a.N], a.plan[kLpUsed]);
     const int total = total_stages(a, steps), per = lora_share(total, a.ctas, least);
     const int cut = (share + 1) * per;
-    if (cut >= total)
+    if (cut >= total) {
+        grid_dep_wait();
         return;
+    }
     const Item it = locate(a, steps, cut);
     const int c0 = it.first / per, c1 = (it.first + it.len - 1) / per;
-    if (it.first == cut)
+    if (it.first == cut) {
+        grid_dep_wait();
         return;
+    }
     const int rank = a.rank[it.e], width = a.p[it.p].width;
     const float alpha = a.p[it.p].scaled ? a.scale[it.e] : 1.0f;
     const size_t slot = kOuterN * (size_t)a.h_cols;
