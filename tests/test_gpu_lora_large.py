@@ -167,3 +167,30 @@ def check_norms(b):
     ([(0, 2000), (1, 1100)], [8, 40], 1536, 2048), ([(1, 1300), (0, 1000)], [128, 70], 2048, 1024)])
 def test_small_values_keep_their_bits(groups, ranks, fin, fout, sizes):
     check_norms(Large(groups, ranks, fin, fout, "f16", seed=len(ranks), **sizes).run("null"))
+
+
+def _spread(n, rows):
+    return [(e, rows + 7 * (e % 5) - 14) for e in range(n)]
+
+
+# Shares of many stages (wide inputs), of many tiles (128 wide: the buffers of h
+# and the first product's accumulators) and of many short items (hundreds of
+# adapters: the gradients' accumulators), at ranks up to 16, 64 and 128.
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("groups,ranks,fin,fout", [
+    ([(0, 3000), (1, 5192)], [64, 128], 5120, 1536),
+    ([(0, 3000), (1, 5192)], [60, 33], 1536, 5120),
+    (_spread(16, 1024), [16] * 16, 5120, 1536),
+    ([(0, 61000), (1, 39001)], [16, 9], 128, 128),
+    ([(0, 61000), (1, 39001)], [64, 40], 128, 256),
+    ([(0, 61000), (1, 39001)], [128, 70], 256, 128),
+    (_spread(200, 40), [100, 128, 3, 90] * 50, 2048, 2048),
+    (_spread(200, 40), [64, 50, 3, 33] * 50, 2048, 1024),
+])
+def test_large_batches(groups, ranks, fin, fout, dtype):
+    b = Large(groups, ranks, fin, fout, dtype, seed=fin + len(ranks), shuffle=len(ranks) == 16).run()
+    check(b, floor=2.0 ** -36 if dtype == "f16" else None)
+    first = [t.clone() for t in b.outputs()]
+    b.run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(first, b.outputs()))
