@@ -373,3 +373,27 @@ def test_feeds_the_expert_layer():
         assert X.exl3_workspace_error(ws) == 0
         outs.append(out)
     assert torch.equal(*outs) and torch.isfinite(outs[0]).all() and outs[0].abs().max() > 0
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [192, 40])
+def test_small_probabilities_have_fp32s_precision(E, renorm):
+    """Logits on a grid of 1/64, so that l - m is exact, and the chosen ones about ten apart: weights
+    down to 1e-33.  What is left to round: exp (1 ulp = 2 * 2^-24), the sum s (V + 5 additions), a
+    division (1), with renorm a second sum (5) and division (1): 24 * 2^-24 with V = 6 and exp's own
+    error in s.  A gradient adds sums of products of the same kind and three roundings."""
+    k, M, eps = 8, 400, 2.0 ** -24
+    g = torch.Generator().manual_seed(E)
+    z = torch.randint(-90 * 64, -85 * 64, (M, E), generator=g).float() / 64
+    gaps = torch.randint(9 * 64, 11 * 64, (M, k), generator=g).float() / 64
+    at = torch.argsort(torch.rand(M, E, generator=g), dim=1)[:, :k]
+    z.scatter_(1, at, 3.0 - torch.cumsum(gaps, dim=1) + gaps[:, :1])
+    d_rw = torch.randn(M, k, generator=g).cuda()
+    z = z.cuda()
+    got = Call(z, k, "f32", renorm, d_rw=d_rw, balance=False, backward=True)
+    ref = oracle(_f64(z), k, renorm, None, _f64(d_rw))
+    assert np.array_equal(got.ids.cpu().numpy(), ref["ids"])
+    off = np.abs(_f64(got.rw) - ref["rw"])
+    assert np.all(off <= 24 * eps * ref["rw"]), f"weights: {(off / ref['rw']).max() / eps:.1f} * 2^-24"
+    off = np.abs(_f64(got.dl) - ref["dl"])
+    assert np.all(off <= 48 * eps * ref["size"] + 1e-44), f"gradients: {(off / (ref['size'] + 1e-40)).max() / eps:.1f} * 2^-24"

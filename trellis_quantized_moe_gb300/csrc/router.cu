@@ -44,16 +44,6 @@ EXL3_DEV void store_float(void *p, size_t i, int dtype, float v)
         static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 2^x, to about two ulps; 0 below the normal range.
-EXL3_DEV float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // The expert of a lane's value i.
 EXL3_DEV int expert_of(int i) { return 64 * (i / 2) + 2 * (threadIdx.x & 31) + (i & 1); }
 
@@ -327,11 +317,11 @@ __global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_f
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            l[i] = exp2_approx((l[i] - ref) * kLog2e);
+            l[i] = expf(l[i] - ref);
             s += l[i];
         }
         s = warp_sum(s);
-        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);    // s is 0 or in [1, E]
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
         if (a.stats && lane == 0)
             reinterpret_cast<float2 *>(a.stats)[t] = make_float2(ref, s);
         if (ok) {
@@ -345,7 +335,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_f
             choose.next(j, out);
         const uint2 mine = choose.collect(k, out);
         const int id = (int)mine.y;
-        float w = lane < k ? exp2_approx((key_logit(C::key(mine.x)) - ref) * kLog2e) * inv : 0.0f;
+        float w = lane < k ? expf(key_logit(C::key(mine.x)) - ref) * inv : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(w);
             w = total == 0.0f ? 0.0f : w / total;
@@ -539,11 +529,11 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 4 : 1) k_router_back
         const Row r = next;
         if (t + step < a.M)
             fetch(t + step, next);
-        const bool some = r.st.y != 0.0f;          // else a row of -inf only: p = 0
+        const float inv = r.st.y == 0.0f ? 0.0f : 1.0f / r.st.y;       // 0: a row of -inf only, p = 0
         if (a.d_rw) {
             float add = r.d;
             if (a.renorm) {                        // w_j (d_j - sum w d), beside the softmax's own term
-                const float pj = r.id >= 0 && some ? exp2_approx((r.chosen - r.st.x) * kLog2e - __log2f(r.st.y)) : 0.0f;
+                const float pj = r.id >= 0 ? expf(r.chosen - r.st.x) * inv : 0.0f;
                 const float total = warp_sum(pj);
                 const float w = total == 0.0f ? 0.0f : pj / total;
                 const float wd = warp_sum(r.id >= 0 ? w * r.d : 0.0f);
@@ -553,8 +543,6 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 4 : 1) k_router_back
                 at[r.id] = add;
             __syncwarp();
         }
-        // p = exp(l - m) / s = 2^((l - m) log2 e - log2 s)
-        const float ls = -__log2f(r.st.y);
         float p[V], own[V];                        // absent experts: nothing stored, not in any sum
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
@@ -563,13 +551,9 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 6 ? 4 : 1) k_router_back
                                    : make_float2(0.0f, 0.0f);
             own[i] = at2.x;
             own[i + 1] = at2.y;
-            p[i] = exp2_approx(fmaf(r.raw.get(i) - r.st.x, kLog2e, ls));
-            p[i + 1] = exp2_approx(fmaf(r.raw.get(i + 1) - r.st.x, kLog2e, ls));
+            p[i] = expf(r.raw.get(i) - r.st.x) * inv;
+            p[i + 1] = expf(r.raw.get(i + 1) - r.st.x) * inv;
         }
-        if (!some)
-#pragma unroll
-            for (int i = 0; i < V; i++)
-                p[i] = 0.0f;
         // sum of p_e x_e over the row's experts
         auto expectation = [&](const float (&x)[V]) {
             float v = 0.0f;
