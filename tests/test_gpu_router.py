@@ -397,3 +397,14 @@ def test_small_probabilities_have_fp32s_precision(E, renorm):
     assert np.all(off <= 24 * eps * ref["rw"]), f"weights: {(off / ref['rw']).max() / eps:.1f} * 2^-24"
     off = np.abs(_f64(got.dl) - ref["dl"])
     assert np.all(off <= 48 * eps * ref["size"] + 1e-44), f"gradients: {(off / (ref['size'] + 1e-40)).max() / eps:.1f} * 2^-24"
+
+
+def test_bool_mask_of_valid_rows():
+    z = _logits(40, 16, "bf16", 5)
+    valid = torch.arange(40, device="cuda") % 3 != 1
+    d_loss = torch.ones(1, device="cuda")
+    a, b = (Call(z, 3, valid=v, d_loss=d_loss, backward=True) for v in (valid, valid.to(torch.uint8)))
+    for n in ("ids", "rw", "counts", "loss", "dl"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    with pytest.raises(ValueError):
+        Call(z, 3, valid=valid.to(torch.int32))

@@ -366,6 +366,11 @@ def _shaped(what, t, shape, dtype=None):
                          f"{'' if dtype is None else ' of ' + str(dtype)}")
 
 
+def _as_bytes(mask):
+    """A bool mask's bytes, 0 and 1."""
+    return mask.view(torch.uint8) if mask is not None and mask.dtype is torch.bool else mask
+
+
 def exl3_router_forward(logits, ids, rw, renorm=False, stats=None, valid=None, counts=None, loss=None,
                         workspace=None, stream=None, raise_on_error=True) -> int:
     M, E = logits.shape
@@ -378,8 +383,8 @@ def exl3_router_forward(logits, ids, rw, renorm=False, stats=None, valid=None, c
     if counts is not None or loss is not None:
         _shaped("counts", counts, (E + 1,), torch.int32)
         _shaped("loss", loss, (1,), torch.float32)
-    if valid is not None:
-        _shaped("valid", valid, (M,), torch.uint8)
+    valid = _as_bytes(valid)
+    _shaped("valid", valid, (M,), torch.uint8)
     rc = _lib.exl3_router_forward(logits.data_ptr(), _DTYPE[logits.dtype], M, E, topk, renorm,
                                   ids.data_ptr(), rw.data_ptr(), _DTYPE[rw.dtype], _ptr(stats),
                                   _ptr(valid), _ptr(counts), _ptr(loss), _ptr(workspace),
@@ -397,8 +402,8 @@ def exl3_router_backward(logits, ids, stats, d_logits, renorm=False, d_rw=None, 
     _shaped("d_logits", d_logits, (M, E), logits.dtype)
     if d_rw is not None:
         _shaped("d_rw", d_rw, (M, topk))
-    if valid is not None:
-        _shaped("valid", valid, (M,), torch.uint8)
+    valid = _as_bytes(valid)
+    _shaped("valid", valid, (M,), torch.uint8)
     if counts is not None or d_loss is not None:
         _shaped("counts", counts, (E + 1,), torch.int32)
         _shaped("d_loss", d_loss, (1,), torch.float32)
