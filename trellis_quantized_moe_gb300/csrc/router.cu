@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32, V <= 12 ? 2 : 1) k_router_f
             choose.next(j, out);
         const uint2 mine = choose.collect(k, out);
         const int id = (int)mine.y;
-        float w = lane < k ? expf(key_logit(C::key(mine.x)) - ref) * inv : 0.0f;
+        // (a division of its own: one rounding less than a product with inv)
+        float w = lane < k && s != 0.0f ? expf(key_logit(C::key(mine.x)) - ref) / s : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(w);
             w = total == 0.0f ? 0.0f : w / total;
