@@ -234,7 +234,7 @@ int exl3_linear_noalloc_error(int32_t *err_host, cudaStream_t stream);
  * in training the balance loss and the gradient of the logits.
  *
  * Per row t: m_t = max_e l_te, s_t = sum_e exp(l_te - m_t), p_te =
- * exp(l_te - m_t) / s_t.  S_t = the
+ * exp(l_te - m_t) / s_t, in fp32.  S_t = the
  * topk largest logits, descending, ties to the lower expert (-0 equals +0, a
  * NaN orders as -inf).  rw_tj = p at S_tj, or (renorm) that divided by the
  * sum of p over S_t.  An expert of logit -inf has p = 0; a row of -inf only has
@@ -253,6 +253,7 @@ size_t exl3_router_workspace_bytes(int M, int E);
  *   backward pass needs it; a sum log s_t + m_t would lose s_t for large m_t).
  *   counts: int32 [E+1] = c_0..c_{E-1}, T; loss: f32 [1]: both or neither.
  *   valid: u8 [M] or NULL.  workspace: only with counts (else NULL, 0).
+ *   M * topk is below 2^30; logits (and d_logits below) are 16-byte aligned.
  *   Sums run in a fixed order: the same call gives the same bits. */
 int exl3_router_forward(const void *logits, int logits_dtype, int M, int E, int topk, int renorm,
                         int32_t *ids, void *rw, int rw_dtype, float *stats, const uint8_t *valid,

@@ -1,6 +1,6 @@
 // Adapters, second product: y[perm[s]][n] = base[perm[s]][n] + alpha * sum_j
 // h[s][j] W_a[j][n] over the rows grouped by adapter (h B forward, dh A
-// backward), with h = the sum of the shrink kernel's partials.
+// backward), with h in two parts as k_lora_join leaves it.
 //
 // Bound by reading base and writing y once (2 r products per 4 bytes).  An
 // item is a tile of 128 rows x 128 outputs; a CTA takes a contiguous share of

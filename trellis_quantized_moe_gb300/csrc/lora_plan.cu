@@ -6,6 +6,11 @@
 // counts, then every warp writes its chunk's rows at its own cursors.  Equal
 // ids inside a 32-row step are ranked by __match_any_sync.  Once per batch,
 // not per projection, so its latency is shared by every adapted projection.
+//
+// Bound by latencies: each warp reads its ids twice, one 32-row step after the
+// other.  Graph replay, int32 ids, one adapter / 40 / 1024: 1 row 10 / 11 / 12 us, 64
+// rows 11 / 15 / 13, 1000 rows 11 / 17 / 19, 16384 rows 19 / 41 / 55, 65536 rows 48 /
+// 118 / 159.
 #include "common.cuh"
 #include "lora.h"
 

@@ -13,10 +13,14 @@
 // and renormalised weights w, which depend on the chosen logits only, add
 // w_i (d_i - sum_j w_j d_j) at the chosen experts.
 //
+// exp is expf and divisions are true ones: with 2^x of a rounded product and
+// approximate reciprocals and logarithms fp32 results were up to twice as far from 64
+// bits as the formula in fp32 (65536 x 192, forward and backward: 51 us so, 56 now).
+//
 // What bounds it: not HBM but the instructions per row, most of them the
-// choice's.  Measured at 65536 x 192 bf16, top 8: forward with the balance 29 us
-// (346 instructions a row, 75% of the issue slots, the ALU pipe 58% busy, DRAM
-// 11%), join 5 us, backward 21 us (232 instructions a row).
+// choice's.  Measured at 65536 x 192 bf16, top 8, graph replay: forward with the
+// balance and its join 32 us (399 instructions a row, 74% of the issue slots, the
+// ALU pipe 54% busy, DRAM 10%), backward 19 us (278 instructions a row).
 #include <type_traits>
 
 #include "common.cuh"
@@ -142,8 +146,11 @@ EXL3_DEV void sort_network(Swap swap)
 }
 
 // The row's experts in order of choice, one call per round: every lane keeps
-// its own experts sorted (a network of V log^2 V exchanges on registers, no
-// branches) and shows the first; the owner of the warp's best moves up.
+// its own experts sorted (a network of V log^2 V exchanges without branches) and
+// shows the first; the owner of the warp's best moves up.  The network lies in
+// registers up to V = 12; at 16 and 32 (more than 384 experts) the compiler keeps
+// its loops, and the keys are in local memory (64 to 624 bytes a thread, with
+// what spills).
 template <bool PACKED, int V>
 struct Chooser;
 
@@ -621,8 +628,10 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
 {
     const size_t bal_smem = ((size_t)a.E + 1 + (size_t)kRouterWarps * a.E) * 4;
     if (!a.counts) {
-        // four warps (192 experts, with 16 / 4 / 1: 100 rows 2.3 / 2.0 / 2.0 us,
-        // 5000 rows 4.2 / 4.0 / 5.6, 20000 rows 10.7 / 9.5 / 10.7)
+        // four warps (192 experts, with 16 / 4 / 1: 100 rows 1.7 / 1.6 / 1.7 us,
+        // 5000 rows 3.7 / 3.3 / 5.5, 20000 rows 8.8 / 8.4 / 10.3).  Registers let 8 to
+        // 10 of the 16 CTAs run at a time, so that above some 6000 rows the grid's
+        // last wave is partly empty.
         constexpr int kW = 4;
         const int need = (a.M + kW - 1) / kW, most = a.num_sms * (64 / kW);
         return launch(k_router_forward<DT, V, false>, need < most ? need : most, kW * 32, 0, s, a);
@@ -633,10 +642,12 @@ cudaError_t forward(const RouterArgs &a, cudaStream_t s)
     return n == 1 || e != cudaSuccess ? e : launch(k_router_join, kJoin, kJoinThreads, 0, s, a, n);
 }
 
+// Four CTAs an SM run at a time up to 192 experts; wider rows take 84 registers
+// and more, so that three and fewer do and a large batch ends in a part of a wave.
 template <int DT, int V>
 cudaError_t backward(const RouterArgs &a, cudaStream_t s)
 {
-    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 4;     // one wave
+    const int need = (a.M + kBackWarps - 1) / kBackWarps, most = a.num_sms * 4;     // one wave up to 192 experts
     return launch(k_router_backward<DT, V>, need < most ? need : most, kBackWarps * 32,
                   (size_t)kBackWarps * ((a.E + 1) / 2 * 2) * 4, s, a);
 }

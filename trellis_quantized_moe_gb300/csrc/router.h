@@ -29,8 +29,9 @@ struct RouterArgs {
 constexpr int kRouterCtas = 304;
 constexpr int kRouterWarps = 16;
 // Balance of at most this many rows: one CTA does it all, two rows a warp, with
-// no second kernel (288 experts, forward and backward: 16 rows 7.6 us; 48 rows
-// 12.5 so and 12.0 with the join, 64 rows 15.2 and 11.9, 128 rows 25.0 and 12.2).
+// no second kernel (288 experts, fp32, the forward pass: 16 rows 4.5 us, 32 rows
+// 7.1; 48 rows 9.6 so and 8.6 with the join, 64 rows 12.1 and 8.6, 128 rows 22.2
+// and 8.6).
 constexpr int kRouterOneCta = 32;
 
 inline int router_balance_ctas(int M)
