@@ -43,7 +43,7 @@
  *     call with the same arguments performs them.
  *   - A negative return is a contract violation found on the host; nothing
  *     was written to device memory and nothing was launched.
- *   - Contracts that only the device can check (route ids in [0, E), each
+ *   - Contracts that only the device can check (route ids in their range, each
  *     expert table entry: K in 1..8, codebook in range, non-null 16-byte
  *     aligned pointers) set a sticky error word in the workspace (see
  *     exl3_workspace_error); later kernels of the call then skip their work and
@@ -90,7 +90,7 @@ enum exl3_status {
 
 /* Device error word bits (exl3_workspace_error). */
 enum exl3_device_error {
-    EXL3_DERR_ROUTE_ID = 1,   /* a route id outside [0, E) */
+    EXL3_DERR_ROUTE_ID = 1,   /* a route id outside [0, E), where the call takes it also not -1 */
     EXL3_DERR_TABLE = 2,      /* a used expert / stage table entry is invalid */
     EXL3_DERR_TIMEOUT = 4,    /* a bounded wait on an asynchronous copy gave up */
     EXL3_DERR_PLAN = 8        /* an adapter plan made for another M or N, or never made */
@@ -185,7 +185,11 @@ int exl3_linear(const void *x, int act_dtype, int M, const exl3_proj *proj, void
  * exllamav3 #284 "Summary"): route packing, per route r = (t, j) with
  * e = ids[t][j]: g = gate_e(x_t), u = up_e(x_t), h = silu(g) * u,
  * d = down_e(h); out[t] = sum_j rw[t][j] * d_{t,j}.
- *   x: [M][hidden] act_dtype (f16/bf16); ids: [M][topk] int32/int64;
+ *   x: [M][hidden] act_dtype (f16/bf16); ids: [M][topk] int32/int64 in [0, E),
+ *   or -1: no route (padding, a route over an expert's capacity, the rows behind
+ *   the last one of exl3_dispatch).  It adds nothing and its rw is not read; a
+ *   token without routes gets zeros, and its row of x is not read.  Also in
+ *   exl3_moe_additive, not in exl3_route_pack.
  *   rw: [M][topk] f16/bf16/f32; out: [M][hidden] act_dtype.
  *   capacity: routes per span tile; results do not depend on it.
  *   workspace: >= exl3_moe_workspace_bytes(...), 256-byte aligned; its
@@ -347,10 +351,10 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
 
 /* ---------------------------------------------------------------- dispatch and combine
  * Tokens in expert order and back, for what runs expert by expert between them:
- * exl3_moe_forward with topk = 1 on the sorted rows (each expert's own output
- * for each route), exl3_linear on an expert's rows, adapters of every expert
- * (exl3_lora_* with `experts` as ids).  R = M * topk is below 2^30 and topk at
- * most EXL3_ROUTER_MAX_TOPK; f = t*topk + j is route j of token t.  Every
+ * exl3_moe_forward with topk = 1 on the sorted rows and `experts` as ids (each
+ * expert's own output for each route), exl3_linear on an expert's rows, adapters of
+ * every expert (exl3_lora_* with `experts` as ids).  R = M * topk is below 2^30
+ * and topk at most EXL3_ROUTER_MAX_TOPK; f = t*topk + j is route j of token t.  Every
  * buffer in expert order holds R rows; of these only the first offsets[E] are
  * read or written.  width is a multiple of 8, M * width below 2^38, and rows are
  * 16-byte aligned. */

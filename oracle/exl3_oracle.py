@@ -307,7 +307,7 @@ def moe_forward(x: np.ndarray, ids: np.ndarray, rw: np.ndarray, get_proj,
     trellis/suh/svh/scale/K/codebook, p in (0 gate, 1 up, 2 down).
     get_residuals(e, p) -> [(alpha, trellis, K)] additive mcg stages.
     tokens: optional subset of rows to evaluate (each row depends only on its
-    own routes).  Returns float64 [len(tokens), H].
+    own routes).  ids of -1: no route.  Returns float64 [len(tokens), H].
     """
     M, topk = ids.shape
     tokens = np.arange(M) if tokens is None else np.asarray(tokens)
@@ -315,6 +315,8 @@ def moe_forward(x: np.ndarray, ids: np.ndarray, rw: np.ndarray, get_proj,
     by_expert = {}
     for i, t in enumerate(tokens):
         for j in range(topk):
+            if ids[t, j] == -1:
+                continue
             by_expert.setdefault(int(ids[t, j]), []).append((i, t, j))
     contrib = {}
     for e, members in sorted(by_expert.items()):
@@ -327,5 +329,6 @@ def moe_forward(x: np.ndarray, ids: np.ndarray, rw: np.ndarray, get_proj,
             contrib[(i, j)] = d[k]
     for i, t in enumerate(tokens):
         for j in range(topk):          # j ascending
-            out[i] += float(rw[t, j]) * contrib[(i, j)]
+            if ids[t, j] != -1:
+                out[i] += float(rw[t, j]) * contrib[(i, j)]
     return out

@@ -296,8 +296,12 @@ int run_moe(const void *x, int act_dtype, int M, int hidden, int inter, int E, i
     g.s_trellis = rp.s_trellis;
     g.s_scale = rp.s_scale;
     g.s_K = rp.s_K;
+    g.ids = ids;
+    g.ids_dtype = ids_dtype;
     g.topk = topk;
     g.M_tokens = M;
+    g.cnt_comb = reinterpret_cast<int32_t *>(w + L.cnt);
+    g.out = out;
 
     // gate/up: [R][2][hidden] -> SwiGLU -> rotated down inputs [R][inter]
     g.in_f = hidden;
@@ -341,8 +345,6 @@ int run_moe(const void *x, int act_dtype, int M, int hidden, int inter, int E, i
     g.packed = rp.packed;
     g.rw = rw;
     g.rw_dtype = rw_dtype;
-    g.cnt_comb = reinterpret_cast<int32_t *>(w + L.cnt);
-    g.out = out;
     // prefill regime: down items stage their rotated rows; the weighted
     // combine follows as one pass in token order
     if ((tc_ok && launch_tc_down(g, maps2, sms, s) != cudaSuccess) ||

@@ -179,6 +179,12 @@ cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, size_t
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Whether flat route f is one (the fused layer's ids, checked; -1: none).
+EXL3_DEV bool has_route(const void *ids, int ids_dtype, size_t f)
+{
+    return ids_dtype == EXL3_I64 ? static_cast<const int64_t *>(ids)[f] >= 0 : static_cast<const int32_t *>(ids)[f] >= 0;
+}
+
 // Bounded wait: gives up after ~2^31 cycles and reports false.
 EXL3_DEV bool mbar_wait(uint64_t *bar, uint32_t parity)
 {

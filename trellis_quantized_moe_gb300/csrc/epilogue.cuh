@@ -76,7 +76,8 @@ __device__ __forceinline__ void epi_down_consts(const GemmArgs &a, int e, int nb
 
 // down: d = Hb(z)*svh*scale into the fp32 staging row of flat route f; the
 // warp that completes all topk routes of a token's block combines them in j
-// order (fp32 fma chain, rounded once) and resets the block's counter.
+// order (fp32 fma chain, rounded once) and resets the block's counter, which
+// start_dropped sets ahead by the token's dropped routes.
 __device__ __forceinline__ void epi_down_row(const GemmArgs &a, int e, int nbk, int prow,
                                              float z[4])
 {
@@ -93,6 +94,7 @@ __device__ __forceinline__ void epi_down_row(const GemmArgs &a, int e, int nbk, 
         z[i] = z[i] * kInvSqrt128 * sv[i] * sc[i];
     const int f = a.packed[prow];
     const int tok = f / a.topk;
+    const bool dropped = a.hdr[kHdrDropped] != 0;
     *reinterpret_cast<float4 *>(a.stage + (size_t)f * a.out_f + col) =
         make_float4(z[0], z[1], z[2], z[3]);
     __threadfence();
@@ -105,6 +107,8 @@ __device__ __forceinline__ void epi_down_row(const GemmArgs &a, int e, int nbk, 
         __threadfence();
         float o4[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < a.topk; j++) {
+            if (dropped && !has_route(a.ids, a.ids_dtype, (size_t)tok * a.topk + j))
+                continue;                    // its staging row holds nothing
             const float w = load_act(a.rw, (size_t)tok * a.topk + j, a.rw_dtype);
             const float4 d = __ldcg(reinterpret_cast<const float4 *>(
                 a.stage + ((size_t)tok * a.topk + j) * a.out_f + col));

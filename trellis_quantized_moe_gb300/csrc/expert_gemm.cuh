@@ -505,6 +505,28 @@ __device__ __forceinline__ int zs_index(int e, int frag)
     return (p * ROWS + row) * kZsLd + col;
 }
 
+// Where the plan counts dropped routes: the counters of the down epilogue's
+// combine start at a token's dropped routes, and a token without any other, which
+// no epilogue reaches, is zero.  By the whole gate/up grid, a warp a token, as its
+// last act, where it costs the items no registers.
+inline __device__ __noinline__ void start_dropped(const void *ids, int ids_dtype, int tokens, int topk,
+                                                  int32_t *cnt_comb, uint16_t *out, int hidden)
+{
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kThreads / 32);
+    for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < tokens; t += warps) {
+        int missing = 0;
+        for (int j0 = 0; j0 < topk; j0 += 32) {
+            const int j = j0 + lane;
+            missing += __popc(__ballot_sync(0xffffffffu, j < topk && !has_route(ids, ids_dtype, (size_t)t * topk + j)));
+        }
+        for (int i = lane; i < hidden / kHb; i += 32)
+            cnt_comb[t * (hidden / kHb) + i] = missing;
+        if (missing == topk)
+            for (int i = lane * 8; i < hidden; i += 256)
+                *reinterpret_cast<uint4 *>(out + (size_t)t * hidden + i) = make_uint4(0, 0, 0, 0);
+    }
+}
+
 template <int MODE, int NRB, bool ADD>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NRB, ADD)) k_expert_gemm(GemmArgs a)
 {
@@ -546,8 +568,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NRB, ADD)) k_expert_gemm
         split = a.hdr[MODE == kModeGateUp ? kHdrSplit1 : kHdrSplit2] != 0;
     }
     const bool work = (int)blockIdx.x < n_items;
-    if (MODE != kModeDown && !work)
+    if (MODE != kModeDown && !work) {
+        if (MODE == kModeGateUp && a.hdr[kHdrDropped] != 0)
+            start_dropped(a.ids, a.ids_dtype, a.M_tokens, a.topk, a.cnt_comb, static_cast<uint16_t *>(a.out), a.in_f);
         return;
+    }
 
     Ring ring;
     ring.bar = bars + warp * kSlots;
@@ -833,6 +858,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NRB, ADD)) k_expert_gemm
         named_barrier(1, kThreads);
     }
     ring_drain(ring);
+    if (MODE == kModeGateUp && a.hdr[kHdrDropped] != 0)
+        start_dropped(a.ids, a.ids_dtype, a.M_tokens, a.topk, a.cnt_comb, static_cast<uint16_t *>(a.out), a.in_f);
 }
 
 template <int MODE, int NRB, bool ADD>

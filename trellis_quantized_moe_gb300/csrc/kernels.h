@@ -26,7 +26,7 @@ struct RoutePackArgs {
     int32_t *offsets, *packed, *tiles, *info;
     int32_t *zero;                  // words to clear (per-call counters), or null
     int nzero;
-    // fused-layer planning (plan != 0)
+    // fused-layer planning (plan != 0; an id of -1 is a route that there is not)
     int plan;
     void *rg;                       // int4 [max_rg] = (expert, first row, rows, 0)
     int nb1, nb2, nchunks1, nchunks2, split_pairs1, split_pairs2, num_sms;
@@ -41,7 +41,8 @@ struct RoutePackArgs {
 struct RotateArgs {
     const void *x;
     int act_dtype, rows, width, nproj;
-    // fused layer: row i is packed slot i, token = packed[i] / topk, suh from the table
+    // fused layer: row i is packed slot i, token = packed[i] / topk, suh from the table;
+    // the plan's dropped routes have no row
     const int32_t *packed;
     const void *ids;
     int ids_dtype, topk;
@@ -98,6 +99,8 @@ struct GemmArgs {
     // gate/up [R][2][inter] (packed order: rotated gate, rotated up)
     float *stage;
     const int32_t *packed;
+    const void *ids;                // read where the plan counts dropped routes
+    int ids_dtype;
     int topk;
     const void *rw;
     int rw_dtype;

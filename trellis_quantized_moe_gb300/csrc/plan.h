@@ -32,6 +32,7 @@ enum HdrWord {
     kHdrNItems1 = 6,
     kHdrNItems2 = 7,
     kHdrRegime = 8,    // fused layer: 0 = decode-regime kernels run, 1 = prefill (tcgen05) kernels
+    kHdrDropped = 9,   // fused layer: routes of -1, behind the last packed slot
     kHdrWords = 64
 };
 

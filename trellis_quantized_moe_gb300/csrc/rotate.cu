@@ -11,6 +11,13 @@ namespace exl3 {
 constexpr int kBlocksPerWarp = 8;
 constexpr int kFeat = kRotFeat;
 
+// Rows there are: in the fused layer all but the dropped routes'.
+template <bool FUSED>
+__device__ __forceinline__ int live_rows(const RotateArgs &a)
+{
+    return FUSED && a.packed ? a.rows - a.hdr[kHdrDropped] : a.rows;
+}
+
 // TRIGGER: the tcgen05 linear, launched after this kernel with programmatic
 // dependent launch, may start once every CTA of this grid is running (its
 // activation producer waits for this grid's completion).  A separate
@@ -34,9 +41,9 @@ __global__ void __launch_bounds__(256) k_rotate(RotateArgs a)
     const int grp = (int)(wg % ngroups);
     const int p = (int)((wg / ngroups) % a.nproj);
     const int row0 = (int)(wg / ((long)ngroups * a.nproj)) * RPW;
-    if (row0 >= a.rows)
+    if (row0 >= live_rows<!TRIGGER>(a))
         return;
-    const int nr = min(RPW, a.rows - row0);
+    const int nr = min(RPW, live_rows<!TRIGGER>(a) - row0);
     const int blk = grp * kBlocksPerWarp + (lane >> 2);
     const int c = lane & 3;                      // quarter of the block
     const bool active = blk < nblk;              // uniform within each group of 4 lanes
@@ -146,9 +153,9 @@ __global__ void __launch_bounds__(kRingWarps * 32, 4) k_rotate_ring(RotateArgs a
     const int grp = (int)(wg % ngroups);
     const int p = (int)((wg / ngroups) % a.nproj);
     const int row0 = (int)(wg / ((long)ngroups * a.nproj)) * a.rpw;
-    if (row0 >= a.rows)
+    if (row0 >= live_rows<!TRIGGER>(a))
         return;
-    const int nr = min(a.rpw, a.rows - row0);
+    const int nr = min(a.rpw, live_rows<!TRIGGER>(a) - row0);
     const int blk = grp * kBlocksPerWarp + (lane >> 2);
     const int c = lane & 3;
     const bool active = blk < nblk;

@@ -8,6 +8,9 @@
 // pass 2 walks each chunk in order, 32 routes at a time, ranking equal ids
 // inside the step with __match_any_sync.  The result is the unique stable
 // order (ascending flat route index inside each expert's span).
+//
+// In the fused layer an id of -1 is a route that there is not: it gets no slot,
+// and its token combines the others.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -138,12 +141,15 @@ __global__ void __launch_bounds__(32, 1) k_route_pack_warp(RoutePackArgs a)
     const int E = a.E, R = a.R, lane = threadIdx.x;
     for (int i = lane; i < a.nzero; i += 32)
         a.zero[i] = 0;
-    const bool valid = lane < R;
-    const long long id = valid ? static_cast<long long>(ids[lane]) : -1;
+    const long long id = lane < R ? static_cast<long long>(ids[lane]) : -1;
+    const unsigned dropped = __ballot_sync(0xffffffffu, a.plan && lane < R && id == -1);
+    const bool valid = lane < R && !(dropped >> lane & 1u);
     if (lane == 0) {
         a.info[kHdrError] = 0;
-        if (a.plan)
+        if (a.plan) {
             a.info[kHdrRegime] = 0;
+            a.info[kHdrDropped] = __popc(dropped);
+        }
     }
     if (__any_sync(0xffffffffu, valid && (id < 0 || id >= E))) {
         if (lane == 0) {
@@ -236,8 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_pack(RoutePackArgs a)
     if (tid == 0) {
         s_err = 0;
         a.info[kHdrError] = 0;
-        if (a.plan)
+        if (a.plan) {
             a.info[kHdrRegime] = 0;
+            a.info[kHdrDropped] = 0;
+        }
     }
     __syncthreads();
 
@@ -247,10 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_pack(RoutePackArgs a)
     const int f_begin = warp * per_warp * 32;
     const int f_end = min(R, f_begin + per_warp * 32);
 
-    // pass 1: validate and count
+    // pass 1: validate and count (fused layer: -1 is no route)
     if (warp < nw) {
         for (int f = f_begin + lane; f < f_end; f += 32) {
             long long e = read_id(ids, f);
+            if (a.plan && e == -1)
+                continue;
             if (e < 0 || e >= E)
                 s_err = 1;
             else
@@ -340,8 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_pack(RoutePackArgs a)
             run += c;
         }
     }
-    if (tid == 0)
+    if (tid == 0) {
         a.offsets[E] = total;
+        if (a.plan)
+            a.info[kHdrDropped] = R - total;
+    }
     __syncthreads();
 
     // pass 2: stable placement
@@ -349,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_pack(RoutePackArgs a)
         const unsigned lt = (1u << lane) - 1u;
         for (int f0 = f_begin; f0 < f_end; f0 += 32) {
             const int f = f0 + lane;
-            const bool valid = f < f_end;
+            const int e = f < f_end ? (int)read_id(ids, f) : -1;
+            const bool valid = e >= 0;
             const unsigned vmask = __ballot_sync(0xffffffffu, valid);
-            int e = valid ? (int)read_id(ids, f) : -1;
             unsigned peers = __match_any_sync(0xffffffffu, e);
             if (valid) {
                 peers &= vmask;

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) k_tc_combine(GemmArgs a)
 {
     if (a.hdr[kHdrRegime] != 1)
         return;
-    const bool err = a.hdr[kHdrError] != 0;
+    const bool err = a.hdr[kHdrError] != 0, dropped = a.hdr[kHdrDropped] != 0;
     const int h4 = a.out_f / 4;
     const size_t n = (size_t)a.M_tokens * h4;
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(256) k_tc_combine(GemmArgs a)
         float o4[4] = {0.f, 0.f, 0.f, 0.f};
         if (!err) {
             for (int j = 0; j < a.topk; j++) {
+                if (dropped && !has_route(a.ids, a.ids_dtype, (size_t)t * a.topk + j))
+                    continue;                    // its staging row holds nothing
                 const float wj = load_act(a.rw, (size_t)t * a.topk + j, a.rw_dtype);
                 const float4 d = __ldcs(reinterpret_cast<const float4 *>(
                     a.stage + ((size_t)t * a.topk + j) * a.out_f + c));
