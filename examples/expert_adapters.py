@@ -10,7 +10,8 @@ each expert's own can stand beside them:
   -> back to the tokens with the route weights (exl3_combine)
 
 and backward through the same steps; one AdamW step (exl3_adamw) moves the
-adapters (float16 with float32 masters and 8-bit states), another the router.
+adapters (float16 with float32 masters and 8-bit states, rounded at random),
+another the router.
 
   python examples/expert_adapters.py          # a short fine-tuning run
 """
@@ -69,7 +70,7 @@ class ExpertAdapted:
         scales = lambda: [torch.zeros(-(-p.numel() // 256), device="cuda") for p in params]
         flat = lambda ts: [t.view(-1) for t in ts]
         self.opt = X.DeviceAdamW(flat(params), flat(grads), codes(), codes(), m_scale=scales(), v_scale=scales(),
-                                 master=flat(masters))
+                                 master=flat(masters), rounding="random")
         zero = lambda: [torch.zeros(H * E, device="cuda")]
         self.opt_router = X.DeviceAdamW(flat([self.router]), flat([self.d_router]), zero(), zero())
         self.step, self.step_router = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))

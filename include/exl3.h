@@ -96,7 +96,8 @@ enum exl3_device_error {
     EXL3_DERR_PLAN = 8        /* an adapter plan made for another M or N, or never made */
 };
 
-enum exl3_dtype { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_F32 = 2, EXL3_I32 = 3, EXL3_I64 = 4, EXL3_E4M3 = 5 };
+enum exl3_dtype { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_F32 = 2, EXL3_I32 = 3, EXL3_I64 = 4, EXL3_E4M3 = 5,
+                  EXL3_E4M3_RANDOM = 6 };     /* e4m3 that the call rounds at random (optimiser states) */
 enum exl3_codebook { EXL3_CB_MUL1 = 0, EXL3_CB_MCG = 1, EXL3_CB_3INST = 2 };
 enum exl3_projection { EXL3_GATE = 0, EXL3_UP = 1, EXL3_DOWN = 2 };
 
@@ -410,12 +411,23 @@ int exl3_combine_backward(const void *d_out, const void *y, int dtype, int M, in
  * rounded copy and not read), else the parameter, rounded once to its type (a
  * 16-bit parameter without a master loses updates below half a step of its type).
  * 8-bit states: per EXL3_ADAMW_BLOCK elements of a tensor one scale = (largest
- * |value|) / 448 and a code e4m3 per element, rounded to the nearest, of
- * m / scale, and in the place of v of sqrt(v) / scale (twice v's range); a
- * sqrt(v) above zero has a code above zero; an m whose block holds nothing above
- * 2^-117 is zero.  The step uses m and v before they are rounded.  fp32 rounds
- * some eight times on the way (a code is the nearest up to 2^-20 of the
- * quotient); the same inputs give the same bits in any grouping of tensors.
+ * |value|) / 448 and a code e4m3 per element, of m / scale, and in the place of v
+ * of sqrt(v) / scale (twice v's range); a sqrt(v) above zero has a code above
+ * zero; an m whose block holds nothing above 2^-117 is zero.  The step uses m and
+ * v before they are rounded.  Codes are rounded
+ *   - EXL3_E4M3: to the nearest.  Each step is exact to half a code, but over
+ *     many steps codes stall: beta2 = 0.999 lets sqrt(v) fall by 0.05% a step,
+ *     a code is 6 to 12% wide, and so an element's v follows its block's largest
+ *     value, not its own gradients.  5000 steps after half of the gradients shrank
+ *     20-fold (grew 4-fold) sqrt(v) is 7.4 (0.87) times what float32 states hold on
+ *     average for these, and 0.81 (3.0) times for the others.  An m stays where it
+ *     is below 5 * 2^-9 (beta1 = 0.9), or at up to 10/8 of a power of two (0.95).
+ *     For some hundred steps, or gradients that keep their sizes.
+ *   - EXL3_E4M3_RANDOM: to one of the two neighbours, with the probability that
+ *     keeps the mean; the same runs stay within 1.01 to 1.03 times.  The
+ *     random bits depend on *step and the element's place in its tensor alone.
+ * fp32 rounds some eight times on the way (what is rounded to a code is known up to
+ * 2^-20 of it); the same inputs give the same bits in any grouping of tensors.
  * A gradient that is infinite or NaN makes its m, v and p NaN or infinite (with
  * 8-bit states an infinite one the states of its whole block): scale and check
  * gradients that may overflow (grad_scale). */
@@ -427,7 +439,7 @@ typedef struct exl3_adamw_tensors {
     const int64_t *param;     /* [N] param_dtype */
     const int64_t *grad;      /* [N] grad_dtype */
     const int64_t *m;         /* [N] state_dtype */
-    const int64_t *v;         /* [N] state_dtype; e4m3: codes of sqrt(v) */
+    const int64_t *v;         /* [N] state_dtype; e4m3 codes: of sqrt(v) */
     const int64_t *m_scale;   /* [N] f32 [ceil(numel / 256)] with e4m3 states, else NULL */
     const int64_t *v_scale;
     const int64_t *master;    /* [N] f32, or NULL: none */
@@ -437,7 +449,7 @@ typedef struct exl3_adamw_tensors {
     int32_t N;
     int32_t param_dtype;      /* f16/bf16/f32 */
     int32_t grad_dtype;       /* param_dtype or f32 */
-    int32_t state_dtype;      /* EXL3_F32 or EXL3_E4M3 */
+    int32_t state_dtype;      /* EXL3_F32, EXL3_E4M3 or EXL3_E4M3_RANDOM */
 } exl3_adamw_tensors;
 
 /* Bytes of workspace exl3_adamw needs (256-byte aligned, need not be initialised;

@@ -11,5 +11,5 @@ from .binding import (  # noqa: F401
     exl3_lora_h_cols, exl3_lora_plan, exl3_lora_plan_bytes, exl3_lora_workspace_bytes,
     exl3_router_backward, exl3_router_forward, exl3_router_workspace_bytes, DeviceAdamW, exl3_adamw,
     exl3_adamw_workspace_bytes, exl3_combine, exl3_combine_backward, exl3_dispatch, exl3_dispatch_plan,
-    exl3_dispatch_workspace_bytes, EXL3_E4M3, EXL3_F16, EXL3_BF16, EXL3_F32, EXL3_I32, EXL3_I64,
+    exl3_dispatch_workspace_bytes, EXL3_E4M3, EXL3_E4M3_RANDOM, EXL3_F16, EXL3_BF16, EXL3_F32, EXL3_I32, EXL3_I64,
 )

@@ -15,7 +15,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libexl3_gb300.so")
 
-EXL3_F16, EXL3_BF16, EXL3_F32, EXL3_I32, EXL3_I64, EXL3_E4M3 = 0, 1, 2, 3, 4, 5
+EXL3_F16, EXL3_BF16, EXL3_F32, EXL3_I32, EXL3_I64, EXL3_E4M3, EXL3_E4M3_RANDOM = 0, 1, 2, 3, 4, 5, 6
 EXL3_CB_MUL1, EXL3_CB_MCG, EXL3_CB_3INST = 0, 1, 2
 STATUS = {0: "OK", -1: "E_NULL", -2: "E_DEVICE", -3: "E_DTYPE", -4: "E_SHAPE", -5: "E_ALIGN",
           -6: "E_WORKSPACE", -7: "E_ROUTING", -8: "E_CODEBOOK", -9: "E_CUDA",
@@ -357,10 +357,12 @@ class DeviceAdamW:
     of one dtype, their gradients (of that dtype or float32) and the states m
     and v, float32 or float8_e4m3fn.  e4m3 states need m_scale and v_scale (one
     float32 per 256 elements; v then holds codes of sqrt(v)); master: float32
-    copies of 16-bit parameters.  Zeroed states are a fresh optimiser's.  Keeps
-    the tensors alive; their storage must stay where it is."""
+    copies of 16-bit parameters.  rounding, of e4m3 states: "nearest", or "random" for
+    runs of more than some hundred steps, over which only that one's moments follow
+    the gradients.  Zeroed states are a fresh optimiser's.  Keeps the tensors alive;
+    their storage must stay where it is."""
 
-    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None):
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, rounding="nearest"):
         opt = lambda l: None if l is None else list(l)
         self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
         self.m_scale, self.v_scale, self.master = opt(m_scale), opt(v_scale), opt(master)
@@ -372,6 +374,8 @@ class DeviceAdamW:
         codes = state is torch.float8_e4m3fn
         if codes == (self.m_scale is None) or codes == (self.v_scale is None):
             raise ValueError("m_scale and v_scale belong to float8_e4m3fn states")
+        if rounding not in ("nearest", "random") or (rounding == "random" and not codes):
+            raise ValueError("rounding is nearest or, of float8_e4m3fn states, random")
         if self.master is not None and p0.dtype is torch.float32:
             raise ValueError("float32 parameters have no masters")
         grad = self.grads[0].dtype if self.grads else None
@@ -400,7 +404,7 @@ class DeviceAdamW:
                         ptrs(self.v_scale), ptrs(self.master), table(numel), table(first)]
         self._struct = exl3_adamw_tensors(*[_ptr(t) for t in self._tables], first[-1], len(numel),
                                           _DTYPE[p0.dtype], _DTYPE[grad],
-                                          EXL3_E4M3 if codes else EXL3_F32)
+                                          EXL3_F32 if not codes else EXL3_E4M3_RANDOM if rounding == "random" else EXL3_E4M3)
         self._ref = ctypes.byref(self._struct)
 
     def struct(self) -> exl3_adamw_tensors:

@@ -12,7 +12,9 @@
 // 42 instructions an element, two cycles of three issue).  Warps take few blocks and
 // there are as many CTAs as that needs: the loads of new CTAs then meet the stores
 // of old ones in long runs (245M elements of a 16-byte pattern without arithmetic:
-// 7.0 TB/s so, 6.0 to 6.7 with persistent CTAs whatever their copies).
+// 7.0 TB/s so, 6.0 to 6.7 with persistent CTAs whatever their copies).  Rounding at
+// random is bound by instructions: 245M elements 1.13, 20M elements 1.4 times as long
+// as to the nearest.
 #include <cuda_fp8.h>
 #include <type_traits>
 
@@ -29,6 +31,22 @@ constexpr int kWarps = kThreads / 32;
 constexpr float kTop = 448.0f;          // largest e4m3 value
 constexpr float kTopInv = 1.0f / 448.0f;
 constexpr float kLeast = 0.001953125f;  // smallest above zero, 2^-9
+
+// Random bits that depend on the step and on an element's place in its tensor
+// alone, so that they are the same in every grouping, replay and grid: the high half
+// of a product with an odd constant folded into the low one, a few times over.  The
+// constants are the first 32 bits of the fractions of the golden ratio and of the
+// roots of 2, 3, 11 and 17 (odd ones).  Words of 512 elements over 8192 steps and of
+// 65536 over 64: mean, chi-square of 1024 bins, counts of rare values, correlations
+// between steps, between elements and across both as of independent ones.
+constexpr uint32_t kGolden = 0x9e3779b9u, kRoot2 = 0x6a09e667u, kRoot3 = 0xbb67ae85u, kRoot11 = 0x510e527fu,
+                   kRoot17 = 0x1f83d9abu;
+
+EXL3_DEV uint32_t fold(uint32_t x, uint32_t odd)
+{
+    const uint64_t p = (uint64_t)x * odd;
+    return (uint32_t)(p >> 32) ^ (uint32_t)p;
+}
 
 EXL3_DEV bool bad_pointer(const int64_t *table, int i, int align)
 {
@@ -58,6 +76,7 @@ __global__ void __launch_bounds__(kBeginThreads) k_adamw_begin(AdamwArgs a)
         s.root = 1.0f / sqrtf(second);
         s.grad = gs;
         s.second = gs * sqrtf(a.c2);
+        s.seed = fold(fold((uint32_t)now ^ kGolden, kRoot2), kRoot3);
     }
     for (int i = (int)threadIdx.x - 32; i < t.N; i += kBeginThreads - 32) {
         if (i < 0)                                  // the first warp
@@ -186,6 +205,18 @@ struct Raw {
     }
 };
 
+// The e4m3 value next to y at or below |y|, or the one above it with the
+// probability that keeps the mean: 20 random bits added below the last one that is
+// kept.  Below 2^-6 codes are a fixed 2^-9 apart, which adding 2^-6 makes the
+// floats' own spacing.  (The type's conversion with random bits takes 16 of them, and
+// beta2 = 0.9999 moves a root by 2^-11 of a code's width.)  A NaN stays one.
+EXL3_DEV float rounded_at_random(float y, uint32_t bits20)
+{
+    const float a = fabsf(y), up = a < 0.015625f ? 0.015625f : 0.0f;
+    const float low = __uint_as_float((__float_as_uint(a + up) + bits20) & 0xfff00000u) - up;
+    return a < 512.0f ? copysignf(low, y) : y;
+}
+
 // The largest |value| of the warp's 256, NaNs left out: bit patterns of floats above zero order as integers.
 EXL3_DEV float block_top(const float (&v)[8])
 {
@@ -242,7 +273,7 @@ EXL3_DEV void wait_copies(int n)
 
 // What a warp does: its blocks' arrays go to shared memory of its own, so that
 // loads in flight cost no registers and a block's end needs no branches in them.
-template <int PT, int GT, bool CODES, bool MASTER>
+template <int PT, int GT, bool CODES, bool MASTER, bool RANDOM>
 struct Warp {
     using Grad = Raw<GT>;
     using Weight = Raw<MASTER ? EXL3_F32 : PT>;
@@ -298,7 +329,8 @@ struct Warp {
     // 32 bits beta2 itself, an error of which would be 1 / (1 - beta2) times as
     // large in a v of many steps.
     template <bool FULL>
-    EXL3_DEV static void step(const AdamwArgs &a, const char *stage, const Arrays &t, int j, int rem, int lane)
+    EXL3_DEV static void step(const AdamwArgs &a, const char *stage, const Arrays &t, int64_t block, int j, int rem,
+                              int lane)
     {
         const int n = FULL ? 8 : min(8, max(0, rem - lane * 8));
         const int at = j * kAdamwBlock + lane * 8;
@@ -371,6 +403,18 @@ struct Warp {
                     vf[k] = y > 0.0f ? fmaxf(y, kLeast) : y;
                 }
             }
+            if constexpr (RANDOM) {
+                const int64_t b = block + j;
+                uint32_t s = fold(a.out->seed ^ (uint32_t)b, kRoot2) + (uint32_t)(b >> 32) + lane * kGolden;
+                s = fold(s, kRoot3);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    // 20 bits each, eight of them the high ones of the first, the low ones of the second
+                    const uint32_t w = fold(fold(s + k * kGolden, kRoot11) ^ s, kRoot17);
+                    mf[k] = rounded_at_random(mf[k], w & 0xfffffu);
+                    vf[k] = rounded_at_random(vf[k], w >> 12);
+                }
+            }
             if (lane % 16 == 0)
                 (lane == 0 ? t.m_scale : t.v_scale)[j] = some ? mine * kTopInv : 0.0f;
         }
@@ -381,10 +425,10 @@ struct Warp {
     }
 };
 
-template <int PT, int GT, bool CODES, bool MASTER>
+template <int PT, int GT, bool CODES, bool MASTER, bool RANDOM>
 __global__ void __launch_bounds__(kThreads, 4) k_adamw(AdamwArgs a)
 {
-    using W = Warp<PT, GT, CODES, MASTER>;
+    using W = Warp<PT, GT, CODES, MASTER, RANDOM>;
     extern __shared__ __align__(16) char stages[];
     grid_dep_wait();
     grid_dep_launch();
@@ -414,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(AdamwArgs a)
             for (int j = 0; j < W::kPer; j++) {
                 wait_copies(W::kPer - 1 - j);
                 __syncwarp();
-                W::template step<true>(a, mine + j * W::kStage, x, j, kAdamwBlock, lane);
+                W::template step<true>(a, mine + j * W::kStage, x, block, j, kAdamwBlock, lane);
             }
         } else {                                    // a tensor's end
 #pragma unroll 1
@@ -427,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(AdamwArgs a)
             for (int j = 0; j < run; j++) {
                 const int rem = left - j * kAdamwBlock;
                 if (rem >= kAdamwBlock)
-                    W::template step<true>(a, mine + j * W::kStage, x, j, rem, lane);
+                    W::template step<true>(a, mine + j * W::kStage, x, block, j, rem, lane);
                 else
-                    W::template step<false>(a, mine + j * W::kStage, x, j, rem, lane);
+                    W::template step<false>(a, mine + j * W::kStage, x, block, j, rem, lane);
             }
         }
         __syncwarp();
@@ -437,18 +481,27 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(AdamwArgs a)
     }
 }
 
-// f(parameter type, gradient type, 8-bit states, masters) as constants
+// f(parameter type, gradient type, 8-bit states, masters, random rounding) as constants
 template <typename F>
 cudaError_t by_kind(const exl3_adamw_tensors &t, F f)
 {
     const auto rest = [&](auto p, auto g) {
         constexpr std::true_type yes;
         constexpr std::false_type no;
-        const bool codes = t.state_dtype == EXL3_E4M3;
+        const auto state = [&](auto master) {
+            switch (t.state_dtype) {
+            case EXL3_E4M3:
+                return f(p, g, yes, master, no);
+            case EXL3_E4M3_RANDOM:
+                return f(p, g, yes, master, yes);
+            default:
+                return f(p, g, no, master, no);
+            }
+        };
         if constexpr (decltype(p)::value != EXL3_F32)
             if (t.master)
-                return codes ? f(p, g, yes, yes) : f(p, g, no, yes);
-        return codes ? f(p, g, yes, no) : f(p, g, no, no);
+                return state(yes);
+        return state(no);
     };
     constexpr std::integral_constant<int, EXL3_F16> f16;
     constexpr std::integral_constant<int, EXL3_BF16> bf16;
@@ -471,15 +524,15 @@ cudaError_t adamw_set_attributes()
     exl3_adamw_tensors t{};
     const int64_t some = 0;
     for (int param = EXL3_F16; param <= EXL3_F32; param++)
-        for (int kind = 0; kind < 8; kind++) {
+        for (int kind = 0; kind < 12; kind++) {
             t.param_dtype = param;
             t.grad_dtype = kind & 1 ? EXL3_F32 : param;
-            t.state_dtype = kind & 2 ? EXL3_E4M3 : EXL3_F32;
-            t.master = kind & 4 ? &some : nullptr;
-            const cudaError_t e = by_kind(t, [](auto p, auto g, auto codes, auto master) {
-                return cudaFuncSetAttribute(k_adamw<p.value, g.value, codes.value, master.value>,
+            t.master = kind & 2 ? &some : nullptr;
+            t.state_dtype = kind < 4 ? EXL3_F32 : kind < 8 ? EXL3_E4M3 : EXL3_E4M3_RANDOM;
+            const cudaError_t e = by_kind(t, [](auto p, auto g, auto codes, auto master, auto random) {
+                return cudaFuncSetAttribute(k_adamw<p.value, g.value, codes.value, master.value, random.value>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            Warp<p.value, g.value, codes.value, master.value>::kSmem);
+                                            Warp<p.value, g.value, codes.value, master.value, random.value>::kSmem);
             });
             if (e != cudaSuccess)
                 return e;
@@ -492,10 +545,10 @@ cudaError_t launch_adamw(const AdamwArgs &a, cudaStream_t s)
     const cudaError_t e = launch_dependent(k_adamw_begin, 1, kBeginThreads, 0, s, a);
     if (e != cudaSuccess || a.t.blocks == 0)
         return e;
-    return by_kind(a.t, [&](auto p, auto g, auto codes, auto master) {
-        using W = Warp<p.value, g.value, codes.value, master.value>;
+    return by_kind(a.t, [&](auto p, auto g, auto codes, auto master, auto random) {
+        using W = Warp<p.value, g.value, codes.value, master.value, random.value>;
         constexpr int kBlocks = kWarps * W::kPer;
-        return launch_dependent(k_adamw<p.value, g.value, codes.value, master.value>,
+        return launch_dependent(k_adamw<p.value, g.value, codes.value, master.value, random.value>,
                                 (int)((a.t.blocks + kBlocks - 1) / kBlocks), kThreads, W::kSmem, s, a);
     });
 }

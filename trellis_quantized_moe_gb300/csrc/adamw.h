@@ -18,6 +18,7 @@ struct AdamwScalars {
     float root;                     // 1 / sqrt(1 - beta2^t)
     float grad;                     // grad_scale
     float second;                   // grad_scale sqrt(1 - beta2)
+    uint32_t seed;                  // of the step's random roundings
 };
 
 struct AdamwArgs {

@@ -18,7 +18,7 @@ int exl3_adamw(const exl3_adamw_tensors *t, double lr, double beta1, double beta
 {
     if (!t || !t->param || !t->grad || !t->m || !t->v || !t->numel || !t->first || !step || !ws)
         return EXL3_E_NULL;
-    const bool codes = t->state_dtype == EXL3_E4M3;
+    const bool codes = t->state_dtype == EXL3_E4M3 || t->state_dtype == EXL3_E4M3_RANDOM;
     if (!is_float_dtype(t->param_dtype) || (t->grad_dtype != t->param_dtype && t->grad_dtype != EXL3_F32) ||
         (!codes && t->state_dtype != EXL3_F32) || (t->master && t->param_dtype == EXL3_F32))
         return EXL3_E_DTYPE;
