@@ -461,8 +461,9 @@ size_t exl3_adamw_workspace_bytes(void);
  *   lr_scale, grad_scale: f32 [1] on the device or NULL (1); a schedule or a
  *   loss scale that changes from one replay of a graph to the next.
  *   step: int32 [1] on the device, steps made so far; the call adds 1.
- *   A grad_scale that is infinite or NaN leaves the step out: nothing is
- *   written, *step stays.  A bad table entry or a *step outside [0, 2^31 - 1)
+ *   A grad_scale that is infinite or NaN, or an lr_scale with which the rate, its
+ *   quotient by 1 - beta1^t or its product with wd is no finite float, leaves the
+ *   step out: nothing is written, *step stays.  A bad table entry or a *step outside [0, 2^31 - 1)
  *   sets EXL3_DERR_TABLE, and nothing else is written. */
 int exl3_adamw(const exl3_adamw_tensors *tensors, double lr, double beta1, double beta2, double eps,
                double weight_decay, const float *lr_scale, const float *grad_scale, int32_t *step,

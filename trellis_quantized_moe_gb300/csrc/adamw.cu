@@ -67,12 +67,12 @@ __global__ void __launch_bounds__(kBeginThreads) k_adamw_begin(AdamwArgs a)
         const double lr = a.lr_scale ? a.lr * (double)*a.lr_scale : a.lr;
         const int32_t made = *a.step;
         bad = t.first[0] != 0 || t.first[t.N] != t.blocks || made < 0 || made == INT32_MAX;
-        s.run = isfinite(gs);
         now = bad ? 1 : made + 1;
         // 1 - beta^t: expm1 keeps its digits where beta^t is near one
         const float first = -expm1f((float)(now * a.log_beta1)), second = -expm1f((float)(now * a.log_beta2));
         s.decay = (float)(1.0 - lr * a.weight_decay);
         s.rate = (float)-lr / first;
+        s.run = isfinite(gs) && isfinite(s.decay) && isfinite(s.rate);
         s.root = 1.0f / sqrtf(second);
         s.grad = gs;
         s.second = gs * sqrtf(a.c2);

@@ -26,7 +26,8 @@ int exl3_adamw(const exl3_adamw_tensors *t, double lr, double beta1, double beta
         return EXL3_E_NULL;
     if (t->N < 1 || t->blocks < 0 || t->blocks >= (1ll << 33))
         return EXL3_E_SHAPE;
-    // what is rounded to float stays in range there; a NaN fails every comparison
+    // what is rounded to float here stays in range there (the rate and its products are
+    // known on the device); a NaN fails every comparison
     const auto scalar = [](double x) { return x >= 0 && x <= 1e30; };
     const auto beta = [](double x) { return x >= 0 && (float)x < 1.0f && (float)(1.0 - x) > 0.0f; };
     if (!scalar(lr) || !scalar(weight_decay) || !scalar(eps) || !((float)eps >= FLT_MIN) || !beta(beta1) || !beta(beta2))
