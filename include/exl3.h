@@ -361,7 +361,8 @@ int exl3_lora_backward(const void *dy, const void *x, const void *h, int act_dty
  * 16-byte aligned. */
 
 /* Bytes of workspace exl3_dispatch_plan needs (256-byte aligned, need not be
- * initialised; its first word is the call's error word).  Calls that may overlap
+ * initialised; its first word is the call's error word).  They never fall as M, topk
+ * or E grows: a workspace of the largest serves all.  Calls that may overlap
  * need workspaces of their own. */
 size_t exl3_dispatch_workspace_bytes(int M, int topk, int E);
 

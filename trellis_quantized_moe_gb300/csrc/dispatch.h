@@ -8,6 +8,8 @@
 namespace exl3 {
 
 constexpr int kPlanCluster = 16;        // CTAs of one cluster at most
+constexpr int kPlanCtas = 128;          // CTAs by themselves at most
+constexpr int kPlanCounts = 65536;      // their counts at most, but one of each
 
 // Threads of a CTA of the plan for R routes.  Few of them where there are few routes:
 // barriers, counters to clear and to add up go by the warps (192 experts, 256 / 512 /
@@ -28,18 +30,21 @@ inline int dispatch_plan_ctas(int R, int E)
             n *= 2;
         return n;
     }
-    const int all = (R + 1023) / 1024, fit = 65536 / (E + 1), most = fit > 128 ? 128 : fit;
+    const int all = (R + 1023) / 1024, fit = kPlanCounts / (E + 1), most = fit > kPlanCtas ? kPlanCtas : fit;
     return all < most ? all : most;
 }
 
 // Workspace: its first word is the call's error word; then int [ctas][E + 2], the
-// CTAs' counts, where they are no cluster.
+// CTAs' counts, where they are no cluster.  The bytes are a bound that never falls
+// as M, topk or E grows, though the CTAs get fewer for many experts: what counts is
+// that ctas (E + 1) <= kPlanCounts and ctas <= kPlanCtas.
 constexpr int kPlanHeader = 64;
 
 inline size_t dispatch_plan_bytes(int R, int E)
 {
-    const int n = dispatch_plan_ctas(R, E);
-    return ((kPlanHeader + (n > kPlanCluster ? (size_t)n * (E + 2) : 0)) * 4 + 255) / 256 * 256;
+    const int n = R <= 32768 ? 0 : R >= kPlanCtas * 1024 ? kPlanCtas : (R + 1023) / 1024;
+    const int all = n * (E + 2), most = kPlanCounts + n;
+    return ((size_t)(kPlanHeader + (all < most ? all : most)) * 4 + 255) / 256 * 256;
 }
 
 struct DispatchPlanArgs {
