@@ -66,7 +66,7 @@ def layer(w, gone, expect=0):
 # and the tcgen05 ones; residual stages
 CASES = [(1, 8, 2, 0, {}), (16, 8, 2, 0, {}), (4, 16, 8, 0, dict(ids="i64", act="bf16")), (32, 8, 1, 0, {}),
          (17, 8, 2, 0, dict(ids="i64")), (64, 8, 2, 0, {}), (128, 64, 32, 0, dict(act="bf16")), (128, 8, 3, 0, {}),
-         (136, 512, 2, 0, dict(ids="i64")), (300, 8, 2, 1, dict(act="bf16")), (300, 8, 1, 1, {}),
+         (136, 512, 2, 0, dict(ids="i64")), (2100, 1024, 2, 0, {}), (300, 8, 2, 1, dict(act="bf16")), (300, 8, 1, 1, {}),
          (2300, 8, 2, 1, dict(ids="i64")), (16, 8, 2, 0, dict(residual=(2,))), (50, 8, 2, 0, dict(residual=(3,))),
          (1100, 8, 2, 1, dict(residual=(2,)))]
 
