@@ -421,8 +421,9 @@ int exl3_combine_backward(const void *d_out, const void *y, int dtype, int M, in
  *     a code is 6 to 12% wide, and so an element's v follows its block's largest
  *     value, not its own gradients.  5000 steps after half of the gradients shrank
  *     20-fold (grew 4-fold) sqrt(v) is 7.4 (0.87) times what float32 states hold on
- *     average for these, and 0.81 (3.0) times for the others.  An m stays where it
- *     is below 5 * 2^-9 (beta1 = 0.9), or at up to 10/8 of a power of two (0.95).
+ *     average for these, and 0.81 (3.0) times for the others.  An m of a gradient
+ *     that stops keeps a code of 1 to 4 times 2^-9 with beta1 = 0.9, also 9/8 and
+ *     10/8 of any power of two with 0.95.
  *     For some hundred steps, or gradients that keep their sizes.
  *   - EXL3_E4M3_RANDOM: to one of the two neighbours, with the probability that
  *     keeps the mean; the same runs stay within 1.01 to 1.03 times.  The

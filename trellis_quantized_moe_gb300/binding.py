@@ -360,7 +360,9 @@ class DeviceAdamW:
     copies of 16-bit parameters.  rounding, of e4m3 states: "nearest", or "random" for
     runs of more than some hundred steps, over which only that one's moments follow
     the gradients.  Zeroed states are a fresh optimiser's.  Keeps the tensors alive;
-    their storage must stay where it is."""
+    their storage must stay where it is: building the tables takes some 2.5 us a
+    tensor, so they are for buffers that stay, and gradients that move from step to
+    step (set to none in between) are copied into such buffers, or get new tables."""
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, rounding="nearest"):
         opt = lambda l: None if l is None else list(l)

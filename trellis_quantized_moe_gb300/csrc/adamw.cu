@@ -13,8 +13,10 @@
 // there are as many CTAs as that needs: the loads of new CTAs then meet the stores
 // of old ones in long runs (245M elements of a 16-byte pattern without arithmetic:
 // 7.0 TB/s so, 6.0 to 6.7 with persistent CTAs whatever their copies).  Rounding at
-// random is bound by instructions: 245M elements 1.13, 20M elements 1.4 times as long
-// as to the nearest.
+// random is bound by instructions: 245M elements 1.13, 20M elements 1.44 times as long
+// as to the nearest.  Of all kinds three spill, one or two registers: f32 parameters
+// with 32-bit states, and 16-bit ones with f32 gradients, masters and codes rounded to
+// the nearest (245M elements: 710 us, 6.2 TB/s).
 #include <cuda_fp8.h>
 #include <type_traits>
 
@@ -54,6 +56,8 @@ EXL3_DEV bool bad_pointer(const int64_t *table, int i, int align)
     return p == 0 || (p & (align - 1)) != 0;
 }
 
+// One CTA: with 1 / 1152 / 3000 / 10000 tensors of a block each a step takes 3.6 / 5.9 /
+// 9.6 / 21 us.
 __global__ void __launch_bounds__(kBeginThreads) k_adamw_begin(AdamwArgs a)
 {
     grid_dep_wait();
@@ -282,9 +286,9 @@ struct Warp {
     static constexpr int kV = kM + kAdamwBlock * State::kBytes, kScales = kV + kAdamwBlock * State::kBytes;
     static constexpr int kStage = kScales + (CODES ? 16 : 0);
     // Blocks of a warp, all on their way at once.  8-bit states: 20M elements with 2 /
-    // 3 / 4 take 42.8 / 41.7 / 41.4 us, 245M with masters 621 / 603 / 626 (and 725
-    // with five CTAs an SM, whose registers spill); 32-bit states: 9.5M elements with
-    // 1 / 2 / 4 took 47.8 / 49.1 / 51.2 us.
+    // 3 / 4 take 42.8 / 41.7 / 41.4 us, 245M with masters 621 / 603 / 626 (before roots
+    // of subnormal v, 611 with them; 725 with five CTAs an SM, whose registers spill);
+    // 32-bit states: 9.5M elements with 1 / 2 / 4 took 47.8 / 49.1 / 51.2 us.
     static constexpr int kPer = CODES ? 3 : 1;
     static constexpr int kSmem = kWarps * kPer * kStage;
 

@@ -15,14 +15,20 @@ namespace exl3 {
 
 namespace {
 
-// With 64 / 128 / 256 threads 8192 x 8 rows of 5120 bf16 combine in 128 / 128 / 137 us.
+// With 64 / 128 / 256 threads 8192 x 8 rows of 5120 bf16 combine in 128 / 128 / 137 us;
+// of other widths, 105M elements in expert order (up to 16384 tokens): 264 wide 20 / 21 / 27, 1032
+// wide 48 / 48 / 50, 1536 wide 40 / 42 / 44, 4096 wide 40 / 40 / 43 us, dispatch 640
+// wide 35 / 31 / 31.  Rows below 1024 elements leave threads idle (128 wide: 2 TB/s).
 constexpr int kThreads = 128;
 // Rows of a token in flight (the same, 2 / 3 / 4 / 5 / 8: 146 / 143 / 128 / 136 / 139 us; one
-// token 2.6 / 2.4 / 2.1 / 2.2 / 2.0).
+// token 2.6 / 2.4 / 2.1 / 2.2 / 2.0; 2 / 4 / 8 of 1536 wide rows 49 / 42 / 45 us, of 4096
+// 46 / 40 / 42).
 constexpr int kBatch = 4;
 constexpr int kRouteWarps = 4;          // routes of a backward CTA
 // Pieces of a route's two rows in flight, for each lane (the backward of the same,
-// 1 / 2 / 4 / 5: 228 / 209 / 208 / 208 us; one token 5.7 / 4.4 / 4.3 / 3.5).
+// 1 / 2 / 4 / 5: 228 / 209 / 208 / 208 us; one token 5.7 / 4.4 / 4.3 / 3.5; 2 / 4 / 5 /
+// 8 of other widths as above: 640 wide 79 / 74 / 79 / 111, 1536 wide 74 / 73 / 75 / 83,
+// 4096 wide 72 / 69 / 70 / 69 us).
 constexpr int kAhead = 5;
 
 // Slot of a route, -1 where it has none (or the table says what no plan says).

@@ -480,12 +480,12 @@ cudaError_t launch_lora_outer(const LoraOuterArgs &a, cudaStream_t s)
     if (a.M > 0) {
         const cudaError_t e =
             launch_dependent(lora::k_lora_outer, a.ctas, lora::kThreads,
-                                   lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s, a);
+                             lora::ring_slots(a.h_cols) * lora::stage_bytes(a.h_cols), s, a);
         if (e != cudaSuccess)
             return e;
     }
     return launch_dependent(lora::k_lora_outer_join, a.ctas * lora::kJoinParts + lora::kZeroBlocks,
-                                  lora::kJoinThreads, 0, s, a);
+                            lora::kJoinThreads, 0, s, a);
 }
 
 cudaError_t lora_set_attributes()

@@ -339,7 +339,7 @@ cudaError_t launch_lora_join(const LoraJoinArgs &a, cudaStream_t s)
 {
     const int tiles = a.M / kLoraTile + (a.N < a.M ? a.N : a.M);       // of adapters, at most
     return launch_dependent(lora::k_lora_join, tiles * (kLoraTile / lora::join_rows(a.h_cols)),
-                                  lora::kJoinThreads, 0, s, a);
+                            lora::kJoinThreads, 0, s, a);
 }
 
 cudaError_t lora_shrink_set_attributes()
