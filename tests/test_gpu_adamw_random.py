@@ -101,6 +101,29 @@ def test_a_gradient_that_is_not_finite_stays_visible(random, bad):
     T.test_a_gradient_that_is_not_finite_stays_visible(True, bad)
 
 
+def test_replays_round_like_eager_steps(random):
+    """The random bits follow the step count on the device, not the capture; another count gives others."""
+    sizes = [30000, 257, 77]
+    a, b = (T.State(sizes, "bf16", codes=True, master=True, seed=2, step=0, fresh=True) for _ in range(2))
+    for s in (a, b):
+        s.go(**T.HYPER)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        b.go(**T.HYPER)
+    for _ in range(5):
+        a.go(**T.HYPER)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert T.same(a.lists(), b.lists()) and int(a.step) == int(b.step) == 6
+    c = T.State(sizes, "bf16", codes=True, master=True, seed=2, step=7)
+    d = T.State(sizes, "bf16", codes=True, master=True, seed=2, step=8)
+    for s in (c, d):
+        s.go(**T.HYPER)
+    torch.cuda.synchronize()
+    assert not torch.equal(c.m[0].view(torch.uint8), d.m[0].view(torch.uint8))
+
+
 class Run:
     """One tensor under the given states, fresh."""
 

@@ -153,6 +153,31 @@ def test_replays_with_changing_drops():
         assert torch.equal(out, fresh) and bool(out.isfinite().all())
 
 
+def test_two_streams_at_once():
+    """Batches with and without drops, each with buffers of its own, over the same experts."""
+    ex, jobs = None, []
+    for M, how in ((24, "some"), (100, None), (900, "last")):
+        w = workload(M, 8, 2)
+        ex = ex or X.DeviceExperts.from_workload(w)
+        if how:
+            drop(w, how, M)
+        s = w.spec
+        buffers = lambda: (out_tensor(w).fill_(float("nan")), torch.full(
+            (X.exl3_moe_workspace_bytes(s.M, s.topk, s.E, s.hidden, s.inter, s.capacity),), 0xFF, dtype=torch.uint8,
+            device="cuda"))
+        jobs.append((moe_inputs(w), s.capacity, torch.cuda.Stream(), buffers(), buffers()))
+    torch.cuda.synchronize()
+    for (x, ids, rw), cap, _, (out, ws), _ in jobs:
+        X.exl3_moe_forward(x, ids, rw, ex, cap, ws, out)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (x, ids, rw), cap, stream, _, (out, ws) in jobs:
+            X.exl3_moe_forward(x, ids, rw, ex, cap, ws, out, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, (alone, _), (out, _) in jobs:
+        assert torch.equal(alone, out) and bool(out.isfinite().all())
+
+
 @pytest.mark.parametrize("M,how", [(12, "some"), (200, "some"), (2300, "last"), (200, "one left"), (200, "all")])
 def test_a_dropped_batch_through_its_experts(M, how):
     """Plan -> dispatch -> the layer on one route a row -> adapters -> combine, and the weights' gradient."""
