@@ -212,8 +212,8 @@ struct Raw {
 // The e4m3 value next to y at or below |y|, or the one above it with the
 // probability that keeps the mean: 20 random bits added below the last one that is
 // kept.  Below 2^-6 codes are a fixed 2^-9 apart, which adding 2^-6 makes the
-// floats' own spacing.  (The type's conversion with random bits takes 16 of them, and
-// beta2 = 0.9999 moves a root by 2^-11 of a code's width.)  A NaN stays one.
+// floats' own spacing.  (beta2 = 0.9999 moves a root by some 2^-11 of a code's width a
+// step, of which 20 bits keep 2^-9.)  A NaN stays one.
 EXL3_DEV float rounded_at_random(float y, uint32_t bits20)
 {
     const float a = fabsf(y), up = a < 0.015625f ? 0.015625f : 0.0f;
